@@ -308,6 +308,228 @@ void bq_sweep_destroy(bq_sweep *plan);
 #define BQ_FLOOR_SINK_WORDS 8192
 int bq_read_floor(const void *p, int64_t bytes, uint32_t *sink, bq_stream s);
 
+/* ------------------------------------------------------------------------
+ * Between the products: the operators that turn the outputs of one group of
+ * products into the activation of the next, for 1 to many tokens at once
+ * (bankML "par.rs -- the persistent thread pool and row scheduler", section
+ * "Summary", counts the 253 products of a token; a decode or prompt step
+ * runs these between them).  All conventions above hold.  Every argument
+ * block is a host struct read during the call; `reserved` fields must be 0.
+ *
+ * Tensors of these calls hold one of three types; a 16-bit result is rounded
+ * once, to nearest even, from f32. */
+#define BQ_F32 0
+#define BQ_F16 1
+#define BQ_BF16 2
+
+/* Residual addition, root-mean-square norm and activation quantizer in one
+ * pass: for each of `tokens` rows of n values,
+ *   h    = x + res, rounded to `type` (x itself where res is NULL)
+ *   r    = 1 / sqrt(sum(h^2) / n + eps), summed and evaluated in binary64
+ *          and rounded once to binary32
+ *   v    = (h * r) * w, each product rounded to binary32
+ *   q, d = the quantizer of bq_quantize_act_q8 on v in blocks of qa (with
+ *          f16_scale that of bq_quantize_act_q8_f16)
+ *   y    = v rounded to `type`
+ * so q and d are the same bits whatever order the sum is taken in (but for a
+ * sum within 2^-50 of where r rounds the other way).  They feed the products
+ * as bq_act {q, d, n, qa, ncols = tokens, ld_q, ld_d}.
+ * x, res, h, w and y hold `type`; rows are ld_* elements apart.  res, h and
+ * y may be NULL (absent); h and y may each be x or res (same pointer and
+ * leading dimension), and not otherwise overlap them.  n is a multiple of
+ * qa, at most BQ_NORM_MAX; qa is 32, 64 or 128; eps > 0.  x, res, h, y and w
+ * are 16-byte aligned, their leading dimensions (and ld_q) multiples of 16
+ * bytes; q is 8-byte aligned with ld_q a multiple of 16, d 4-byte.  tokens =
+ * 0 does nothing.  Non-finite values are outside the contract, as in the
+ * quantizer.  Returns BQ_EARG / BQ_EALIGN before any launch, or BQ_EHIP.
+ * Allocates nothing.  Asynchronous on s. */
+#define BQ_NORM_MAX 65536
+typedef struct bq_norm {
+    int32_t type;      /* BQ_F32, BQ_F16 or BQ_BF16 */
+    int32_t qa;        /* values per scale */
+    int32_t f16_scale; /* 0, or 1: f16-valued scales */
+    float eps;
+    int64_t tokens;
+    int64_t n;
+    const void *x;
+    int64_t ld_x;
+    const void *res;
+    int64_t ld_res;
+    void *h;
+    int64_t ld_h;
+    const void *w;
+    int8_t *q;
+    int64_t ld_q;
+    float *d;
+    int64_t ld_d;
+    void *y;
+    int64_t ld_y;
+} bq_norm;
+int bq_rmsnorm_q8(const bq_norm *a, bq_stream s);
+
+/* A paged cache of keys and values (device, 16-byte aligned, owned by the
+ * caller).  Place p of the cache is offset p % page of page p / page.  Keys
+ * lie as [pages][heads][page][dim]; values as [pages][heads][dim][page], the
+ * tokens of a page side by side for each value index, because the attention
+ * sums over tokens and reads the operand of its matrix products so without
+ * moving it.  Nothing reads a place before a token was written there. */
+typedef struct bq_kv_cache {
+    int32_t type;  /* BQ_F16 or BQ_BF16 */
+    int32_t heads; /* key heads, 1..1024 */
+    int32_t dim;   /* values per head: 64 or 128 */
+    int32_t page;  /* tokens per page: a power of two, 16..256 */
+    int64_t pages; /* 1 <= pages, pages * page < 2^31 */
+    void *k;
+    void *v;
+} bq_kv_cache;
+
+/* New tokens into the cache: for each of `tokens` rows t, every query and
+ * key head is normed (v * (1 / sqrt(mean(v^2) + eps)) * norm weight, where
+ * q_norm / k_norm is not NULL) and rotated by the token's position: for
+ * i < rot / 2 the pair (v[i], v[i + rot/2]) turns by the angle pos[t] *
+ * freq[i] (the angle in binary64, so that far positions keep their phase);
+ * values from rot on stay.  The key row goes to place slot[t] of the cache,
+ * the value row there too (neither normed nor rotated), both rounded to the
+ * cache's type; the query row goes to q_out, in `type` or, with q_out_type,
+ * in the cache's.  A token whose slot is not in [0, pages * page) (-1: padding of the
+ * batch) is not cached; its query row is still written.  Slots that occur
+ * twice in a call leave either token's values there, element by element.
+ * q, k, v and q_out rows hold their heads end to end, rows ld_* elements
+ * apart (q and q_out NULL, q_heads 0: keys and values only); `type` is
+ * BQ_F32 or the cache's type.  rot is 0 or a multiple of 16, at most dim.
+ * pos (int32) and slot (int64) are device arrays of `tokens`, freq (rot / 2
+ * floats), q_norm and k_norm (dim floats) device arrays.  q_out may be q.
+ * Pointers are 16-byte aligned (pos, slot, freq and the weights by their
+ * element), leading dimensions multiples of 16 bytes.  tokens = 0 does
+ * nothing.  Returns BQ_EARG / BQ_EALIGN before any launch, or BQ_EHIP.
+ * Allocates nothing.  Asynchronous on s. */
+typedef struct bq_append {
+    bq_kv_cache cache;
+    int32_t type;       /* of q, k and v */
+    int32_t q_out_type; /* of q_out: `type` or the cache's type */
+    int32_t q_heads;    /* 0..1024 */
+    int32_t rot;
+    float eps; /* > 0 where a norm weight is given */
+    int32_t reserved;
+    int64_t tokens;
+    const void *q;
+    int64_t ld_q;
+    const void *k;
+    int64_t ld_k;
+    const void *v;
+    int64_t ld_v;
+    void *q_out;
+    int64_t ld_qo;
+    const int32_t *pos;
+    const int64_t *slot;
+    const float *freq;
+    const float *q_norm;
+    const float *k_norm;
+} bq_append;
+int bq_kv_append(const bq_append *a, bq_stream s);
+
+/* Causal attention of the new tokens of several requests over the paged
+ * cache that already holds them.  Request b has rows cu[b] .. cu[b+1] - 1 of
+ * q (n of them, any number from 0) and lens[b] = L keys, key j at place
+ * table[b][j / page] * page + j % page; its row i sees the keys j <= L - n + i:
+ *   o = sum_j exp(scale q.k_j - m) v_j / sum_j exp(scale q.k_j - m)
+ * per query head, the q_heads / heads query heads of a key head together.
+ * A row that sees no key (L < n) is 0.  Rows of out at or behind
+ * cu[requests] are left as they were.  One token per request is a decode
+ * step, n = L a whole prompt, anything between a chunk of one.
+ * q and out (q_heads heads of dim end to end, rows ld_* elements apart) hold
+ * `type`: BQ_F32 or the cache's type.  With f32 rows the matrix products run
+ * on the cache's 16-bit type with q and the weights exp(..) split into parts
+ * that carry 22 bits or more, so out is good to f32 sums; with 16-bit rows
+ * the weights are rounded to that type once, which costs as much as rounding
+ * out does.  Softmax statistics and sums are f32.
+ * cu (requests + 1), lens and table (requests rows, ld_table entries apart,
+ * table_cols of them each) are int32 device arrays, so that a captured graph
+ * can be replayed with other lengths; max_new and max_keys (host) bound the
+ * new tokens and keys of any request, and only affect how the work is split
+ * (larger counts are still computed).  What the device arrays say is bounded
+ * in the kernel: rows past `tokens`, keys past table_cols * page and pages
+ * outside the cache are not read (keys of such a page count as unseen).
+ * Places of keys below L must hold finite values; others may hold anything.
+ * work (device, 16-byte aligned, bq_paged_attn_work_bytes bytes, may be NULL
+ * if that is 0) is scratch of this call until it has run: calls that may run
+ * at the same time need one each.  out must not overlap q.  tokens = 0 or
+ * requests = 0 does nothing.  Returns BQ_EARG / BQ_EALIGN before any launch,
+ * or BQ_EHIP.  Allocates nothing.  Asynchronous on s. */
+typedef struct bq_attn {
+    bq_kv_cache cache;
+    int32_t type;    /* of q and out */
+    int32_t q_heads; /* a multiple of cache.heads, at most 16 query heads per key head */
+    int32_t requests;
+    int32_t table_cols;
+    int64_t ld_table;
+    int64_t tokens; /* rows of q and out, < 2^31 */
+    int64_t max_new;
+    int64_t max_keys;
+    const void *q;
+    int64_t ld_q;
+    void *out;
+    int64_t ld_out;
+    const int32_t *cu;
+    const int32_t *lens;
+    const int32_t *table;
+    float scale;
+    int32_t reserved;
+    void *work;
+    int64_t work_bytes;
+} bq_attn;
+int bq_paged_attn(const bq_attn *a, bq_stream s);
+
+/* Bytes of `work` that bq_paged_attn needs for this argument block (its
+ * pointers are not read).  Host only. */
+int bq_paged_attn_work_bytes(const bq_attn *a, int64_t *bytes);
+
+/* Low-rank adapters of many requests beside a shared projection: request b
+ * has rows cu[b] .. cu[b+1] - 1 of x, y and out, and adapter ids[b]:
+ *   out = y + gain[id] * B_id (A_id x)
+ * with A_id (rank x n) at a + id * rank * n and B_id (rows x rank) at
+ * b + id * rows * rank.  A request whose id is not in [0, count) (-1: none)
+ * gets out = y.  Rows at or behind cu[requests] are left as they were.
+ * y and out are f32, as the products write them (column c of
+ * bq_q1_0_matvec's y is row c here); out may be y.  x holds x_type: BQ_F32
+ * or the adapters' type.  Sums are f32; f32 values enter the matrix products
+ * in parts that carry 22 bits or more.
+ * cu (requests + 1) and ids are int32 device arrays, gain f32; max_new
+ * (host) bounds the rows of any request and only affects how the work is
+ * split.  n is a multiple of 8, rank a multiple of 8 up to 128.  x, a, b and
+ * work are 16-byte aligned, ld_x a multiple of 16 bytes; y and out 4-byte.
+ * work (bq_adapters_work_bytes bytes) is scratch of this call until it has
+ * run: calls that may run at the same time need one each.  tokens = 0 or
+ * requests = 0 does nothing.  Returns BQ_EARG / BQ_EALIGN before any launch,
+ * or BQ_EHIP.  Allocates nothing.  Asynchronous on s. */
+typedef struct bq_adapters {
+    int32_t type;   /* of a and b: BQ_F16 or BQ_BF16 */
+    int32_t x_type; /* BQ_F32 or type */
+    int32_t rank;
+    int32_t count;
+    int32_t requests;
+    int32_t reserved;
+    int64_t n;
+    int64_t rows;
+    int64_t tokens;
+    int64_t max_new;
+    const void *a;
+    const void *b;
+    const float *gain;
+    const void *x;
+    int64_t ld_x;
+    const int32_t *cu;
+    const int32_t *ids;
+    const float *y;
+    int64_t ld_y;
+    float *out;
+    int64_t ld_out;
+    void *work;
+    int64_t work_bytes;
+} bq_adapters;
+int bq_adapters_add(const bq_adapters *a, bq_stream s);
+int bq_adapters_work_bytes(const bq_adapters *a, int64_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,6 +32,8 @@ EXPORTS = (
     "bq_quantize_act_q8", "bq_quantize_act_q8_f16", "bq_q1_0_matvec", "bq_q2_0_matvec", "bq_group_matvec",
     "bq_sweep_create", "bq_sweep_create_x", "bq_token_sweep", "bq_sweep_destroy", "bq_read_floor",
     "bq_token_sweep_noalloc", "bq_set_batch_path",
+    "bq_rmsnorm_q8", "bq_kv_append", "bq_paged_attn", "bq_paged_attn_work_bytes", "bq_adapters_add",
+    "bq_adapters_work_bytes",
 )
 
 
@@ -407,3 +409,13 @@ def bq_token_sweep_noalloc(entries, stream=None) -> None:
     scratch holds the plan)."""
     arr = _gemv_list(entries, "bq_token_sweep_noalloc")
     _check(lib.bq_token_sweep_noalloc(arr, len(entries), _stream(stream)))
+
+
+# ------------------------------------- operators between the products (layer.py)
+try:
+    import torch as _torch  # noqa: F401
+except ImportError:  # as in _load: the host calls work without it
+    pass
+else:
+    from .layer import (BQ_BF16, BQ_F16, BQ_F32, BQ_NORM_MAX, Adapters, KVCache, bq_adapters_add,  # noqa: F401
+                        bq_adapters_work_bytes, bq_kv_append, bq_paged_attn, bq_paged_attn_work_bytes, bq_rmsnorm_q8)

@@ -1,0 +1,113 @@
+// bq_half.h -- internal to libbq: the three value types of the operators
+// between the products, their 16-byte loads and stores, and the matrix
+// instructions of the two 16-bit ones.
+//
+// Lane layout of v_mfma_f32_16x16x32 (wavefront lane l): A holds row l % 16,
+// B column l % 16, both at k = 8 (l / 16) + e for element e of the lane's
+// eight; C and D hold rows 4 (l / 16) + i, i < 4, of column l % 16.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "../../include/bq.h"
+#include "bq_types.h"
+
+namespace bq {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int TYPE> struct Num;
+template <> struct Num<BQ_F32> { typedef float t; };
+template <> struct Num<BQ_F16> {
+    typedef _Float16 t;
+    typedef f16x8 v8;
+    static __device__ __forceinline__ f32x4 mfma16(v8 a, v8 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mfma32(v8 a, v8 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+template <> struct Num<BQ_BF16> {
+    typedef __bf16 t;
+    typedef bf16x8 v8;
+    static __device__ __forceinline__ f32x4 mfma16(v8 a, v8 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mfma32(v8 a, v8 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+// Eight consecutive values (16-byte aligned) widened to f32; the store rounds
+// to nearest even.
+template <class T>
+__device__ __forceinline__ void load8(const T *p, float (&v)[8])
+{
+    if constexpr (sizeof(T) == 4) {
+        const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0], b = reinterpret_cast<const f32x4 *>(p)[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = a[e];
+            v[4 + e] = b[e];
+        }
+    } else {
+        typedef T tx8 __attribute__((ext_vector_type(8)));
+        const tx8 a = *reinterpret_cast<const tx8 *>(p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = (float)a[e];
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store8(T *p, const float (&v)[8])
+{
+    if constexpr (sizeof(T) == 4) {
+        f32x4 a, b;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            a[e] = v[e];
+            b[e] = v[4 + e];
+        }
+        reinterpret_cast<f32x4 *>(p)[0] = a;
+        reinterpret_cast<f32x4 *>(p)[1] = b;
+    } else {
+        typedef T tx8 __attribute__((ext_vector_type(8)));
+        tx8 a;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            a[e] = (T)v[e];
+        *reinterpret_cast<tx8 *>(p) = a;
+    }
+}
+
+// Sizes in bytes of the three types.
+inline int type_size(int type) { return type == BQ_F32 ? 4 : 2; }
+
+// The request that row t belongs to, of n requests with rows cu[b] ..
+// cu[b+1] - 1: the last b with cu[b] <= t (requests without rows are skipped
+// by it); n or more, or -1, where no request has the row.
+__device__ __forceinline__ int request_of(const int32_t *cu, int n, int t)
+{
+    if (t < cu[0] || t >= cu[n])
+        return -1;
+    int lo = 0, hi = n;  // cu[lo] <= t < cu[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+}  // namespace bq

@@ -1,0 +1,42 @@
+// bq_layer.h -- internal to libbq: argument blocks and launchers of the
+// operators between the products.  The entry points in bq_layer.cpp check
+// every argument first; the launchers validate nothing and return
+// hipGetLastError().
+#pragma once
+
+#include "../../include/bq.h"
+#include "bq_types.h"
+
+namespace bq {
+
+struct NormArgs {
+    const void *x, *res, *w;
+    void *h, *y;
+    int8_t *q;
+    float *d;
+    int64_t ld_x, ld_res, ld_h, ld_y, ld_q, ld_d;
+    int32_t n, qa;
+    int32_t f16_scale;
+    float eps;
+};
+hipError_t launch_norm(int type, const NormArgs &a, int64_t rows, hipStream_t st);
+
+hipError_t launch_append(const bq_append &a, hipStream_t st);
+
+// How bq_paged_attn splits its work (attn_plan): tiles of 16 nt rows of one
+// key head's queries, `tiles` of them at most per request, each over `chunks`
+// pieces of `chunk` keys that the join adds up.
+struct AttnPlan {
+    int nt;
+    int tiles;
+    int chunks;
+    int chunk;
+    int64_t work_bytes;
+};
+AttnPlan attn_plan(const bq_attn &a);
+hipError_t launch_attn(const bq_attn &a, const AttnPlan &p, hipStream_t st);
+
+int64_t adapters_work(const bq_adapters &a);
+hipError_t launch_adapters(const bq_adapters &a, hipStream_t st);
+
+}  // namespace bq
