@@ -328,11 +328,16 @@ int bq_read_floor(const void *p, int64_t bytes, uint32_t *sink, bq_stream s);
  *   r    = 1 / sqrt(sum(h^2) / n + eps), summed and evaluated in binary64
  *          and rounded once to binary32
  *   v    = (h * r) * w, each product rounded to binary32
- *   q, d = the quantizer of bq_quantize_act_q8 on v in blocks of qa (with
- *          f16_scale that of bq_quantize_act_q8_f16)
+ *   d    = max|v| * (1 / 127) over each block of qa, both in binary32 (with
+ *          f16_scale narrowed to f16, nearest even, as bq_quantize_act_q8_f16
+ *          does), within one unit in the last place of amax / 127
+ *   q    = v / d (correctly rounded) rounded half away from zero, clamped to
+ *          [-127, 127]; d = 0 gives 0
  *   y    = v rounded to `type`
  * so q and d are the same bits whatever order the sum is taken in (but for a
- * sum within 2^-50 of where r rounds the other way).  They feed the products
+ * sum within 2^-50 of where r rounds the other way), the bits that elementwise
+ * tensor operations on the GPU give, which divide by a constant as a product
+ * with its reciprocal.  They feed the products
  * as bq_act {q, d, n, qa, ncols = tokens, ld_q, ld_d}.
  * x, res, h, w and y hold `type`; rows are ld_* elements apart.  res, h and
  * y may be NULL (absent); h and y may each be x or res (same pointer and
@@ -348,7 +353,8 @@ typedef struct bq_norm {
     int32_t type;      /* BQ_F32, BQ_F16 or BQ_BF16 */
     int32_t qa;        /* values per scale */
     int32_t f16_scale; /* 0, or 1: f16-valued scales */
-    float eps;
+    int32_t reserved;
+    double eps;
     int64_t tokens;
     int64_t n;
     const void *x;

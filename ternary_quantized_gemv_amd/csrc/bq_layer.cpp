@@ -155,8 +155,10 @@ BQ_EXPORT int bq_rmsnorm_q8(const bq_norm *a, bq_stream s)
         return set_error(BQ_EARG, "%s: qa %d not in {32, 64, 128}", fn, (int)a->qa);
     if (a->f16_scale != 0 && a->f16_scale != 1)
         return set_error(BQ_EARG, "%s: f16_scale %d is not 0 or 1", fn, (int)a->f16_scale);
-    if (!(a->eps > 0.0f) || !isfinite(a->eps))
-        return set_error(BQ_EARG, "%s: eps %g is not a positive number", fn, (double)a->eps);
+    if (a->reserved != 0)
+        return set_error(BQ_EARG, "%s: reserved must be 0", fn);
+    if (!(a->eps > 0.0) || !isfinite(a->eps))
+        return set_error(BQ_EARG, "%s: eps %g is not a positive number", fn, a->eps);
     int rc = check_tokens(fn, a->tokens);
     if (rc)
         return rc;

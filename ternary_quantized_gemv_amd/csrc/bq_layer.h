@@ -17,7 +17,7 @@ struct NormArgs {
     int64_t ld_x, ld_res, ld_h, ld_y, ld_q, ld_d;
     int32_t n, qa;
     int32_t f16_scale;
-    float eps;
+    double eps;
 };
 hipError_t launch_norm(int type, const NormArgs &a, int64_t rows, hipStream_t st);
 

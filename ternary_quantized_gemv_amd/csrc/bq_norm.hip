@@ -2,7 +2,7 @@
 // quantizer in one pass over a row (bq_rmsnorm_q8).
 //
 // h = round(x + res); r = fl32(1 / sqrt(sum(h^2) / n + eps)); v = fl(fl(h r) w);
-// d = amax|v| / 127 and q = half-away(v / d) per block of qa.  The sum runs in
+// d = max|v| * fl32(1 / 127) and q = half-away(v / d) per block of qa.  The sum runs in
 // binary64 (the squares of f32 values are exact there), so r does not depend
 // on the order of the sum and q, d are reproducible bit for bit; at 2 f64
 // operations per value they are nowhere near a bound.  What bounds it is
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a)
     sum = 0.0;
     for (int k = 0; k < (int)(blockDim.x >> 6); ++k)
         sum += sums[k];
-    const float r = (float)(1.0 / __builtin_sqrt(sum / (double)a.n + (double)a.eps));
+    const float r = (float)(1.0 / __builtin_sqrt(sum / (double)a.n + a.eps));
 #pragma unroll
     for (int c = 0; c < R; ++c) {
         const int i = 8 * (c * (int)blockDim.x + (int)threadIdx.x);
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a)
             m = fmaxf(m, __shfl_xor(m, 8, 64));
         if (i >= a.n)
             continue;
-        float db = m / 127.0f, q[8];
+        float db = m * (1.0f / 127.0f), q[8];
         if (a.f16_scale)
             db = (float)(_Float16)db;
         if (a.f16_scale && db < 0x1p-14f) {

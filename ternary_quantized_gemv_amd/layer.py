@@ -23,7 +23,8 @@ _i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c
 
 
 class bq_norm(ctypes.Structure):
-    _fields_ = [("type", _i32), ("qa", _i32), ("f16_scale", _i32), ("eps", _f32), ("tokens", _i64), ("n", _i64),
+    _fields_ = [("type", _i32), ("qa", _i32), ("f16_scale", _i32), ("reserved", _i32), ("eps", ctypes.c_double),
+                ("tokens", _i64), ("n", _i64),
                 ("x", _vp), ("ld_x", _i64), ("res", _vp), ("ld_res", _i64), ("h", _vp), ("ld_h", _i64), ("w", _vp),
                 ("q", _vp), ("ld_q", _i64), ("d", _vp), ("ld_d", _i64), ("y", _vp), ("ld_y", _i64)]
 
@@ -160,7 +161,7 @@ def bq_rmsnorm_q8(x, w, eps: float, qa: int, q, d, res=None, h=None, y=None, f16
     n = x.shape[-1]
     T = x.shape[0] if x.dim() == 2 else 1
     shape = (T, n)
-    a = bq_norm(kind, qa, int(f16_scale), eps, T, n, *_rows(fn, "x", x, dt, dev, shape),
+    a = bq_norm(kind, qa, int(f16_scale), 0, eps, T, n, *_rows(fn, "x", x, dt, dev, shape),
                 *((None, 0) if res is None else _rows(fn, "res", res, dt, dev, shape)),
                 *((None, 0) if h is None else _rows(fn, "h", h, dt, dev, shape)), _flat(fn, "w", w, dt, dev, n),
                 *_rows(fn, "q", q, torch.int8, dev, shape),

@@ -43,10 +43,17 @@ def norm_ref(x, res, w, eps, qa, f16_scale):
     dt = x.dtype
     h = x if res is None else (x.float() + res.float()).to(dt)
     hf = h.float()
-    r = (1.0 / torch.sqrt(hf.double().square().sum(1) / x.shape[1] + float(np.float32(eps)))).float()
+    r = (1.0 / torch.sqrt(hf.double().square().sum(1) / x.shape[1] + eps)).float()
     v = hf * r[:, None] * w.float()
-    q, d, _ = oracle.quantize_q8(v.numpy().ravel(), qa, f16_scale)
-    return h, v, torch.from_numpy(q).view(v.shape), torch.from_numpy(d).view(v.shape[0], -1)
+    blocks = v.unflatten(1, (-1, qa)).numpy()
+    d = np.abs(blocks).max(2) * (np.float32(1) / np.float32(127))
+    if f16_scale:
+        d = oracle.f32_to_f16(d.ravel()).view(np.float16).astype(np.float32).reshape(d.shape)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        ratio = (blocks / d[..., None]).astype(np.float64)
+    q = np.copysign(np.floor(np.abs(ratio) + 0.5), ratio).clip(-127, 127)
+    q = np.where(d[..., None] == 0, 0, q).astype(np.int8).reshape(v.shape)
+    return h, v, torch.from_numpy(q), torch.from_numpy(d)
 
 
 # ----------------------------------------------------------------- append

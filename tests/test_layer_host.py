@@ -13,7 +13,7 @@ P = 0x10000
 
 
 def norm(**k):
-    a = L.bq_norm(L.BQ_F32, 128, 0, 1e-6, 2, 256, P, 256, P, 256, P, 256, P, P, 256, P, 2, None, 0)
+    a = L.bq_norm(L.BQ_F32, 128, 0, 0, 1e-6, 2, 256, P, 256, P, 256, P, 256, P, P, 256, P, 2, None, 0)
     for n, v in k.items():
         setattr(a, n, v)
     return a
@@ -54,7 +54,7 @@ def rc_of(fn, a):
 
 CASES = [
     ("bq_rmsnorm_q8", norm, [
-        ("type", 3), ("qa", 48), ("f16_scale", 2), ("eps", 0.0), ("eps", float("inf")), ("eps", float("nan")),
+        ("type", 3), ("qa", 48), ("f16_scale", 2), ("reserved", 1), ("eps", 0.0), ("eps", float("inf")), ("eps", float("nan")),
         ("tokens", -1), ("tokens", 1 << 31), ("n", 0), ("n", 200), ("n", 65536 + 128), ("x", None), ("w", None),
         ("q", None), ("d", None), ("ld_x", 255), ("ld_x", 1 << 41), ("ld_res", 128), ("ld_h", 0), ("ld_q", 240),
         ("ld_d", 1)], [
