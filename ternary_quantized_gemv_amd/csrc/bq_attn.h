@@ -1,0 +1,133 @@
+// bq_attn.h -- internal to libbq: what the two attention kernels share
+// (bq_attn.hip: few rows, keys split over wavefronts; bq_attn_tiles.hip: many
+// rows, keys shared through LDS).
+#pragma once
+
+#include "bq_half.h"
+#include "bq_layer.h"
+
+namespace bq {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kNone = -__builtin_inff();
+
+// Parts of an f32 value in 16-bit type T, and the power of two that the
+// weights are scaled by (both in the numerator and in l).
+template <class T> struct Parts { static constexpr int n = 3; static constexpr float up = 0.0f; };
+template <> struct Parts<_Float16> { static constexpr int n = 2; static constexpr float up = 14.0f; };
+
+struct AttnArgs {
+    bq_attn a;
+    AttnPlan p;
+    int group;  // query heads per key head
+    int page_log2;
+};
+
+// Which of the two kernels has a request of this many rows, where both run:
+// the one for many rows has those of more than kFewRows.
+constexpr int kFewRows = 64;
+__device__ __forceinline__ bool has_few(const AttnPlan &p, int rows)
+{
+    return p.many.tiles == 0 || (p.few.tiles && rows <= kFewRows);
+}
+
+// The keys and rows of one request, bounded by what the launch was given.
+struct Request {
+    int row0, n, keys;
+};
+__device__ __forceinline__ Request request_at(const bq_attn &a, int b)
+{
+    Request r;
+    const int lo = a.cu[b], hi = a.cu[b + 1];
+    r.row0 = lo < 0 ? 0 : lo;
+    const int end = hi > a.tokens ? (int)a.tokens : hi;
+    r.n = lo < 0 ? 0 : end - lo;  // a request that starts before the rows is none
+    const int64_t most = (int64_t)a.table_cols * a.cache.page;
+    const int len = a.lens[b];
+    r.keys = len < 0 ? 0 : len > most ? (int)most : len;
+    return r;
+}
+
+// Page of key block `key` (a multiple of 8) of a request, -1 where there is none.
+__device__ __forceinline__ int page_at(const AttnArgs &g, const int32_t *table, int key, int end)
+{
+    if (key >= end)
+        return -1;
+    const int p = table[key >> g.page_log2];
+    return (unsigned)p < (unsigned)g.a.cache.pages ? p : -1;
+}
+
+// One column's query fragments: element e of fragment j is q[at + step j + e].
+// Returns the factor from products with the fragments to log2 units, never
+// negative: a negative scale turns the sign of q instead, so that the largest
+// score is the largest product.  f32 rows come in NP parts; over an f16 cache
+// they are first scaled so that the row's largest value is 2^13 to 2^14
+// (`across` is the maximum over the lanes that share a column).
+template <class T, class v8, int NP, int N, bool F32, class ACROSS>
+__device__ __forceinline__ float load_query(const bq_attn &a, int64_t at, int step, v8 (&f)[NP][N], ACROSS across)
+{
+    const bool neg = a.scale < 0.0f;
+    float factor = fabsf(a.scale) * kLog2e;
+    if constexpr (!F32) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            f[0][j] = *reinterpret_cast<const v8 *>(static_cast<const T *>(a.q) + at + step * j);
+            if (neg)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[0][j][e] = -f[0][j][e];
+        }
+    } else {
+        float x[N][8], top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            load8(static_cast<const float *>(a.q) + at + step * j, x[j]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[j][e] = neg ? -x[j][e] : x[j][e];
+                top = fmaxf(top, fabsf(x[j][e]));
+            }
+        }
+        if constexpr (NP == 2) {
+            top = across(top);
+            int ex = 0;
+            (void)__builtin_frexpf(top, &ex);
+            ex = top > 0.0f ? (ex < -100 ? -100 : ex) : 14;
+            const float up = __builtin_ldexpf(1.0f, 14 - ex);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[j][e] *= up;
+            factor = __builtin_ldexpf(factor, ex - 14);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float rest = x[j][e];
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                    f[p][j][e] = (T)rest;
+                    rest -= (float)f[p][j][e];
+                }
+            }
+    }
+    return factor;
+}
+
+// Where chunk c of row `row` (token * q_heads + head) keeps its part: D sums,
+// then, behind all rows' sums, a maximum and a sum of weights.
+__device__ __forceinline__ float *part_sums(const AttnArgs &g, int64_t row, int c, int dim)
+{
+    return static_cast<float *>(g.a.work) + (row * g.p.stride + c) * dim;
+}
+__device__ __forceinline__ float2 *part_stats(const AttnArgs &g, int64_t row, int c, int dim)
+{
+    float *end = static_cast<float *>(g.a.work) + g.a.tokens * g.a.q_heads * g.p.stride * dim;
+    return reinterpret_cast<float2 *>(end) + row * g.p.stride + c;
+}
+
+hipError_t launch_attn_tiles(const AttnArgs &g, hipStream_t st);
+
+}  // namespace bq

@@ -1,71 +1,35 @@
-// bq_attn.hip -- attention of new tokens over the paged cache (bq_paged_attn).
+// bq_attn.hip -- attention of few new tokens over the paged cache, and the join
+// of split keys (bq_paged_attn; whole prompts and long chunks are in
+// bq_attn_tiles.hip).
 //
 // o_r = sum_j exp(scale q_r.k_j - m_r) v_j / sum_j exp(scale q_r.k_j - m_r) in
 // one pass over the keys, with a running maximum m_r and sum l_r per row.  The
 // rows of one key head are its G query heads of each new token, row r = i G + g
 // of token i: all of them see nearly the same keys, so a key is read once for
-// up to 16 nt rows.
+// up to 16 NT rows.
 //
 // A wavefront takes 32 keys at a time and computes the transposed products
 // S^T = K Q^T and O^T = V^T P^T, rows of the result along keys (values), columns
-// along rows r.  Result row r' = 4 g + i of 16-key tile t is assigned key
+// along rows r.  Result row 4 g + i of 16-key tile t is assigned key
 // 8 g + 4 t + i (g = lane / 16): a lane then holds the scores of keys 8 g .. 8 g
 // + 7 of its column, which is exactly the second product's B operand, and the
 // transposed value pages give its A operand as one 16-byte load.  So scores,
-// weights and sums never leave the lane's registers, and m, l are two values
-// per lane.
+// weights and sums never leave the lane's registers, m and l are two values
+// per lane, and the keys go straight from memory to the matrix cores.
 //
 // f32 rows: q and the weights are split into 16-bit parts whose products with
 // the cache are exact and add up in f32 (three of bf16, 24 bits; two of f16, 22
 // bits, q scaled by a power of two per row).  f16 weights are scaled by 2^14 in
 // either case, so that small ones stay clear of f16's subnormals.
-#include "bq_half.h"
-#include "bq_layer.h"
+//
+// Memory bounds it: 2 D values a key and head, read once.
+#include "bq_attn.h"
 
 namespace bq {
 
 constexpr int kAttnWaves = 4;
 constexpr int kAttnKeys = 32;  // keys of a wavefront at a time
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kNone = -__builtin_inff();
-
-// Parts of an f32 value in 16-bit type T, and the power of two that the
-// weights are scaled by (both in the numerator and in l).
-template <class T> struct Parts { static constexpr int n = 3; static constexpr float up = 0.0f; };
-template <> struct Parts<_Float16> { static constexpr int n = 2; static constexpr float up = 14.0f; };
-
-struct AttnArgs {
-    bq_attn a;
-    AttnPlan p;
-    int group;  // query heads per key head
-    int page_log2;
-};
-
-// The keys and rows of one request, bounded by what the launch was given.
-struct Request {
-    int row0, n, keys;
-};
-__device__ __forceinline__ Request request_at(const bq_attn &a, int b)
-{
-    Request r;
-    const int lo = a.cu[b], hi = a.cu[b + 1];
-    r.row0 = lo < 0 ? 0 : lo;
-    const int end = hi > a.tokens ? (int)a.tokens : hi;
-    r.n = lo < 0 ? 0 : end - lo;  // a request that starts before the rows is none
-    const int64_t most = (int64_t)a.table_cols * a.cache.page;
-    const int len = a.lens[b];
-    r.keys = len < 0 ? 0 : len > most ? (int)most : len;
-    return r;
-}
-
-// Page of key block `key` (a multiple of 8) of a request, -1 where there is none.
-__device__ __forceinline__ int page_at(const AttnArgs &g, const int32_t *table, int key, int end)
-{
-    if (key >= end)
-        return -1;
-    const int p = table[key >> g.page_log2];
-    return (unsigned)p < (unsigned)g.a.cache.pages ? p : -1;
-}
+constexpr int kAttnStep = kAttnKeys * kAttnWaves;
 
 template <int CT, int D, int NT, bool F32>
 __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
@@ -74,24 +38,30 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
     typedef typename Num<CT>::v8 v8;
     constexpr int NP = F32 ? Parts<T>::n : 1;
     constexpr int DJ = D / 32, DT = D / 16;
+    constexpr int REGIONS = NT == 1 ? kAttnWaves : 1;  // few rows: a place per wavefront for its sums
     __shared__ float sm[kAttnWaves][NT][16], sl[kAttnWaves][NT][16];
-    __shared__ float so[NT * 16][D + 4];
+    __shared__ float so[REGIONS][NT * 16][D + 4];
 
     const bq_attn &a = g.a;
+    const AttnSplit &sp = g.p.few;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c16 = lane & 15, q4 = lane >> 4;
-    const int b = blockIdx.z, kh = blockIdx.y;
-    const int tile = blockIdx.x / g.p.chunks, chunk = blockIdx.x % g.p.chunks;
+    const int b = blockIdx.z, kh = blockIdx.x;
+    const int tile = blockIdx.y / sp.chunks, chunk = blockIdx.y % sp.chunks;
     const Request rq = request_at(a, b);
-    if (rq.n <= 0)
+    const int64_t rows64 = (int64_t)rq.n * g.group;
+    if (rq.n <= 0 || !has_few(g.p, (int)rows64))
         return;
-    const int rows = rq.n * g.group;
-    const int64_t page_elems = (int64_t)a.cache.heads << g.page_log2;
-    const T *kbase = static_cast<const T *>(a.cache.k), *vbase = static_cast<const T *>(a.cache.v);
-    const int32_t *table = a.table + (int64_t)b * a.ld_table;
+    const int rows = (int)rows64;
+    const int64_t page_elems = ((int64_t)a.cache.heads << g.page_log2) * D;
     const int P = a.cache.page, pmask = P - 1;
+    const T *kbase = static_cast<const T *>(a.cache.k) + (int64_t)kh * P * D + 8 * q4;
+    const T *vbase = static_cast<const T *>(a.cache.v) + (int64_t)(kh * D + c16) * P;
+    const int32_t *table = a.table + (int64_t)b * a.ld_table;
+    // K: this lane reads key 8 (c16 / 4) + c16 % 4 (+ 4); V: keys 8 q4 .. 8 q4 + 7
+    const int kofs = 8 * (c16 >> 2), vofs = 8 * q4;
 
-    for (int r0 = tile * 16 * NT; r0 < rows; r0 += g.p.tiles * 16 * NT) {
+    for (int r0 = tile * 16 * NT; r0 < rows; r0 += sp.tiles * 16 * NT) {
         // ---- the rows: this lane's columns are rows r0 + 16 t + c16
         v8 qf[NT][NP][DJ];
         float qs[NT], m[NT], l[NT];
@@ -101,51 +71,14 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
             const int r = r0 + 16 * t + c16;
             const bool live = r < rows;
             const int i = live ? r / g.group : 0, hq = kh * g.group + (live ? r % g.group : 0);
-            const int64_t at = (rq.row0 + i) * a.ld_q + (int64_t)hq * D + 8 * q4;
             last[t] = live ? rq.keys - rq.n + i : -1;
             m[t] = kNone;
             l[t] = 0.0f;
-            qs[t] = a.scale * kLog2e;
-            if constexpr (!F32) {
-#pragma unroll
-                for (int j = 0; j < DJ; ++j)
-                    qf[t][0][j] = *reinterpret_cast<const v8 *>(static_cast<const T *>(a.q) + at + 32 * j);
-            } else {
-                float x[DJ][8], top = 0.0f;
-#pragma unroll
-                for (int j = 0; j < DJ; ++j) {
-                    load8(static_cast<const float *>(a.q) + at + 32 * j, x[j]);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        top = fmaxf(top, fabsf(x[j][e]));
-                }
-                if constexpr (NP == 2) {
-                    top = fmaxf(top, __shfl_xor(top, 16, 64));
-                    top = fmaxf(top, __shfl_xor(top, 32, 64));
-                    int ex;
-                    (void)__builtin_frexpf(top, &ex);
-                    ex = top > 0.0f ? ex : 0;
-                    ex = ex < -100 ? -100 : ex;  // the largest value becomes 2^13 .. 2^14
-                    const float up = __builtin_ldexpf(1.0f, 14 - ex > 120 ? 120 : 14 - ex);
-#pragma unroll
-                    for (int j = 0; j < DJ; ++j)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            x[j][e] *= up;
-                    qs[t] /= up;
-                }
-#pragma unroll
-                for (int j = 0; j < DJ; ++j)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float rest = x[j][e];
-#pragma unroll
-                        for (int p = 0; p < NP; ++p) {
-                            qf[t][p][j][e] = (T)rest;
-                            rest -= (float)qf[t][p][j][e];
-                        }
-                    }
-            }
+            qs[t] = load_query<T, v8, NP, DJ, F32>(a, (int64_t)(rq.row0 + i) * a.ld_q + (int64_t)hq * D + 8 * q4, 32, qf[t],
+                                                   [](float x) {
+                                                       x = fmaxf(x, __shfl_xor(x, 16, 64));
+                                                       return fmaxf(x, __shfl_xor(x, 32, 64));
+                                                   });
         }
         f32x4 o[NT][DT];
 #pragma unroll
@@ -157,72 +90,93 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
         // ---- the keys: those that the tile's last row sees, this workgroup's chunk of them
         const int last_row = min(r0 + 16 * NT, rows) - 1;
         const int seen = min(rq.keys, rq.keys - rq.n + last_row / g.group + 1);
-        const int begin = chunk * g.p.chunk;
-        const int end = chunk == g.p.chunks - 1 ? seen : min(seen, begin + g.p.chunk);
+        const int begin = chunk * sp.chunk;
+        const int end = chunk == sp.chunks - 1 ? seen : min(seen, begin + sp.chunk);
         const int first_last = rq.keys - rq.n + r0 / g.group;  // the last key that the tile's first row sees
 
-        for (int k0 = begin + kAttnKeys * wave; k0 < end; k0 += kAttnKeys * kAttnWaves) {
-            const int kk = k0 + 8 * (c16 >> 2), vk = k0 + 8 * q4;
-            const int kp = page_at(g, table, kk, end), vp = page_at(g, table, vk, end);
-            const bool whole = k0 + kAttnKeys - 1 <= first_last && k0 + kAttnKeys <= end && !__any(kp < 0);
-            const T *kr = kbase + (int64_t)max(kp, 0) * page_elems * D + ((int64_t)kh * P + (kk & pmask) + (c16 & 3)) * D +
-                          8 * q4;
-            const T *vr = vbase + (int64_t)max(vp, 0) * page_elems * D + ((int64_t)kh * D + c16) * P + (vk & pmask);
-            v8 kf[2][DJ], vf[DT];
+        // pages one step ahead of the keys, keys and values one product ahead of their use
+        int k0 = begin + kAttnKeys * wave;
+        int kp = page_at(g, table, k0 + kofs, end), vp = page_at(g, table, k0 + vofs, end);
+        v8 kf[2][DJ], vf[DT];
+        auto load_k = [&](int at, int page) {
+            const T *p = kbase + (int64_t)max(page, 0) * page_elems + (((at + kofs) & pmask) + (c16 & 3)) * D;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int j = 0; j < DJ; ++j)
-                    kf[t][j] = *reinterpret_cast<const v8 *>(kr + 4 * t * D + 32 * j);
+                    kf[t][j] = *reinterpret_cast<const v8 *>(p + 4 * t * D + 32 * j);
+        };
+        auto load_v = [&](int at, int page) {
+            const T *p = vbase + (int64_t)max(page, 0) * page_elems + ((at + vofs) & pmask);
 #pragma unroll
             for (int d = 0; d < DT; ++d)
-                vf[d] = *reinterpret_cast<const v8 *>(vr + (int64_t)16 * d * P);
+                vf[d] = *reinterpret_cast<const v8 *>(p + 16 * d * P);
+        };
+        if (k0 < end) {
+            load_k(k0, kp);
+            load_v(k0, vp);
+        }
+        while (k0 < end) {
+            const int next = k0 + kAttnStep;
+            const int nkp = page_at(g, table, next + kofs, end), nvp = page_at(g, table, next + vofs, end);
+            const bool whole = k0 + kAttnKeys - 1 <= first_last && k0 + kAttnKeys <= end && !__any(kp < 0);
+            f32x4 s[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    s[t][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int p = NP - 1; p >= 0; --p)
+#pragma unroll
+                        for (int j = 0; j < DJ; ++j)
+                            s[t][h] = Num<CT>::mfma16(kf[h][j], qf[t][p][j], s[t][h]);
+                }
+            if (next < end)
+                load_k(next, nkp);
             if (!whole) {
                 // places that no row sees may hold anything: their values must not meet a weight of 0
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        vf[d][e] = vk + e < end && vp >= 0 ? vf[d][e] : (T)0.0f;
+                        vf[d][e] = k0 + vofs + e < end && vp >= 0 ? vf[d][e] : (T)0.0f;
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                f32x4 s[2];
+                float w[8], factor = qs[t], top = kNone;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    s[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int e = 0; e < 8; ++e)
+                    w[e] = s[t][e >> 2][e & 3];
+                if (!whole) {
 #pragma unroll
-                    for (int p = NP - 1; p >= 0; --p)
-#pragma unroll
-                        for (int j = 0; j < DJ; ++j)
-                            s[h] = Num<CT>::mfma16(kf[h][j], qf[t][p][j], s[h]);
+                    for (int e = 0; e < 8; ++e) {
+                        const int key = k0 + vofs + e;
+                        w[e] = key <= last[t] && key < end && vp >= 0 ? w[e] * factor : kNone;
+                    }
+                    factor = 1.0f;
                 }
-                float w[8], top = kNone;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    w[e] = s[e >> 2][e & 3] * qs[t];
-                    if (!whole)
-                        w[e] = vk + e <= last[t] && vk + e < end && vp >= 0 ? w[e] : kNone;
+                for (int e = 0; e < 8; ++e)
                     top = fmaxf(top, w[e]);
-                }
                 top = fmaxf(top, __shfl_xor(top, 16, 64));
-                top = fmaxf(top, __shfl_xor(top, 32, 64));
-                const float mn = fmaxf(m[t], top);
-                // nothing seen yet: any finite number will do, all weights are 0
-                const float mz = mn == kNone ? 0.0f : mn;
-                const float f = __builtin_amdgcn_exp2f(m[t] - mz);
-                m[t] = mn;
-                float sum = 0.0f;
+                top = fmaxf(top, __shfl_xor(top, 32, 64)) * factor;
+                if (__any(top > m[t])) {
+                    const float mn = fmaxf(m[t], top);
+                    const float f = __builtin_amdgcn_exp2f(m[t] - (mn == kNone ? 0.0f : mn));
+                    m[t] = mn;
+                    l[t] *= f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    w[e] = __builtin_amdgcn_exp2f(w[e] - mz + Parts<T>::up);
-                    sum += w[e];
+                    for (int d = 0; d < DT; ++d)
+                        o[t][d] *= f;
                 }
-                l[t] = l[t] * f + sum;
+                // nothing seen yet: any finite number will do, all weights are 0
+                const float shift = Parts<T>::up - (m[t] == kNone ? 0.0f : m[t]);
                 v8 pf[NP];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float rest = w[e];
+                    float rest = __builtin_amdgcn_exp2f(__builtin_fmaf(w[e], factor, shift));
+                    l[t] += rest;
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
                         pf[p][e] = (T)rest;
@@ -230,13 +184,16 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
                     }
                 }
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    o[t][d] *= f;
+                for (int d = 0; d < DT; ++d)
 #pragma unroll
                     for (int p = NP - 1; p >= 0; --p)
                         o[t][d] = Num<CT>::mfma16(vf[d], pf[p], o[t][d]);
-                }
             }
+            if (next < end)
+                load_v(next, nvp);
+            k0 = next;
+            kp = nkp;
+            vp = nvp;
         }
         // ---- the four wavefronts' sums become one; l over the lane's key groups first
 #pragma unroll
@@ -249,17 +206,13 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
             }
         }
         __syncthreads();
-        float mt[NT], lt[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            mt[t] = kNone;
+            float mt = kNone;
+#pragma unroll
             for (int w = 0; w < kAttnWaves; ++w)
-                mt[t] = fmaxf(mt[t], sm[w][t][c16]);
-            const float mz = mt[t] == kNone ? 0.0f : mt[t];
-            lt[t] = 0.0f;
-            for (int w = 0; w < kAttnWaves; ++w)
-                lt[t] += sl[w][t][c16] * __builtin_amdgcn_exp2f(sm[w][t][c16] - mz);
-            const float f = __builtin_amdgcn_exp2f(m[t] - mz);
+                mt = fmaxf(mt, sm[w][t][c16]);
+            const float f = __builtin_amdgcn_exp2f(m[t] - (mt == kNone ? 0.0f : mt));
 #pragma unroll
             for (int d = 0; d < DT; ++d)
                 o[t][d] *= f;
@@ -270,32 +223,41 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int d = 0; d < DT; ++d) {
-                        f32x4 *p = reinterpret_cast<f32x4 *>(&so[16 * t + c16][16 * d + 4 * q4]);
-                        *p = w ? *p + o[t][d] : o[t][d];
+                        f32x4 *p = reinterpret_cast<f32x4 *>(&so[REGIONS > 1 ? w : 0][16 * t + c16][16 * d + 4 * q4]);
+                        *p = w && REGIONS == 1 ? *p + o[t][d] : o[t][d];
                     }
             }
-            __syncthreads();
+            if (REGIONS == 1)
+                __syncthreads();
         }
-        // ---- out, or this chunk's part of it: [row][chunk][D] then [row][chunk] of (m, l)
-        const int64_t all_rows = a.tokens * a.q_heads;
-        float *po = static_cast<float *>(a.work);
-        float2 *pm = reinterpret_cast<float2 *>(po + all_rows * g.p.chunks * D);
+        if (REGIONS > 1)
+            __syncthreads();
+        // ---- out, or this chunk's part of it
         for (int u = threadIdx.x; u < 16 * NT * (D / 8); u += 64 * kAttnWaves) {
             const int cr = u / (D / 8), d8 = u % (D / 8) * 8, r = r0 + cr;
             if (r >= rows)
                 continue;
             const int64_t tok = rq.row0 + r / g.group;
             const int hq = kh * g.group + r % g.group;
-            float v[8];
-            load8(&so[cr][d8], v);
-            if (g.p.chunks == 1) {
-                float lt1 = 0.0f, mt1 = kNone;
-                for (int w = 0; w < kAttnWaves; ++w)
-                    mt1 = fmaxf(mt1, sm[w][cr >> 4][cr & 15]);
-                const float mz = mt1 == kNone ? 0.0f : mt1;
-                for (int w = 0; w < kAttnWaves; ++w)
-                    lt1 += sl[w][cr >> 4][cr & 15] * __builtin_amdgcn_exp2f(sm[w][cr >> 4][cr & 15] - mz);
-                const float inv = lt1 > 0.0f ? 1.0f / lt1 : 0.0f;
+            float v[8], mt = kNone, lt = 0.0f;
+            load8(&so[0][cr][d8], v);
+#pragma unroll
+            for (int w = 1; w < REGIONS; ++w) {
+                float x[8];
+                load8(&so[w][cr][d8], x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] += x[e];
+            }
+#pragma unroll
+            for (int w = 0; w < kAttnWaves; ++w)
+                mt = fmaxf(mt, sm[w][cr >> 4][cr & 15]);
+            const float mz = mt == kNone ? 0.0f : mt;
+#pragma unroll
+            for (int w = 0; w < kAttnWaves; ++w)
+                lt += sl[w][cr >> 4][cr & 15] * __builtin_amdgcn_exp2f(sm[w][cr >> 4][cr & 15] - mz);
+            if (sp.chunks == 1) {
+                const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     v[e] *= inv;
@@ -305,54 +267,75 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
                 else
                     store8(static_cast<T *>(a.out) + at, v);
             } else {
-                store8(po + ((tok * a.q_heads + hq) * g.p.chunks + chunk) * D + d8, v);
-            }
-        }
-        if (g.p.chunks > 1 && wave == 0 && q4 == 0) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int r = r0 + 16 * t + c16;
-                if (r < rows) {
-                    const int64_t at = (rq.row0 + r / g.group) * (int64_t)a.q_heads + kh * g.group + r % g.group;
-                    pm[at * g.p.chunks + chunk] = make_float2(mt[t], lt[t]);
-                }
+                store8(part_sums(g, tok * a.q_heads + hq, chunk, D) + d8, v);
+                if (d8 == 0)
+                    *part_stats(g, tok * a.q_heads + hq, chunk, D) = make_float2(mt, lt);
             }
         }
         __syncthreads();
     }
 }
 
-// The chunks of a row added up: D / 8 lanes a row.
+// The pieces of a row added up, one workgroup a row: the lanes of a wavefront
+// hold the pieces' statistics (at most 128), then D / 8 threads take every
+// 256 / (D / 8)-th piece's sums and add up through LDS, always in that order.
+constexpr int kMaxChunks = 128;
+
 template <class OT, int D>
 __global__ __launch_bounds__(256) void attn_join(const AttnArgs g)
 {
     const bq_attn &a = g.a;
-    constexpr int L = D / 8;
-    const int64_t u = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
-    const int d8 = threadIdx.x % L * 8;
-    if (u >= a.tokens * a.q_heads)
-        return;
-    const int64_t tok = u / a.q_heads;
-    const int hq = (int)(u % a.q_heads);
+    constexpr int L = D / 8, GROUPS = 256 / L;
+    __shared__ float weight[kMaxChunks];
+    __shared__ float so[GROUPS][D + 4];
+    const int64_t row = blockIdx.x, tok = row / a.q_heads;
+    const int hq = (int)(row % a.q_heads);
     const int b = request_of(a.cu, a.requests, (int)tok);
     if (b < 0)
         return;
-    const float *po = static_cast<const float *>(a.work);
-    const float2 *pm = reinterpret_cast<const float2 *>(po + a.tokens * a.q_heads * g.p.chunks * D);
-    float m = kNone;
-    for (int c = 0; c < g.p.chunks; ++c)
-        m = fmaxf(m, pm[u * g.p.chunks + c].x);
-    const float mz = m == kNone ? 0.0f : m;
-    float l = 0.0f, o[8] = {};
-    for (int c = 0; c < g.p.chunks; ++c) {
-        const float2 ml = pm[u * g.p.chunks + c];
-        const float f = __builtin_amdgcn_exp2f(ml.x - mz);
+    const int64_t rows = (int64_t)request_at(a, b).n * g.group;
+    const int chunks = has_few(g.p, (int)rows) ? g.p.few.chunks : g.p.many.chunks;
+    if (chunks == 1)
+        return;
+    const int lane = threadIdx.x & 63;
+    const float2 none = make_float2(kNone, 0.0f);
+    const float2 s0 = lane < chunks ? *part_stats(g, row, lane, D) : none;
+    const float2 s1 = lane + 64 < chunks ? *part_stats(g, row, lane + 64, D) : none;
+    float m = fmaxf(s0.x, s1.x);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+        m = fmaxf(m, __shfl_xor(m, off, 64));
+    m = m == kNone ? 0.0f : m;
+    const float f0 = __builtin_amdgcn_exp2f(s0.x - m), f1 = __builtin_amdgcn_exp2f(s1.x - m);
+    float l = s0.y * f0 + s1.y * f1;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+        l += __shfl_xor(l, off, 64);
+    if (threadIdx.x < 64) {
+        weight[lane] = f0;
+        weight[lane + 64] = f1;
+    }
+    __syncthreads();
+    const int grp = threadIdx.x / L, d8 = threadIdx.x % L * 8;
+    float o[8] = {};
+    for (int c = grp; c < chunks; c += GROUPS) {
         float v[8];
-        load8(po + (u * g.p.chunks + c) * D + d8, v);
-        l = __builtin_fmaf(ml.y, f, l);
+        load8(part_sums(g, row, c, D) + d8, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            o[e] = __builtin_fmaf(v[e], f, o[e]);
+            o[e] = __builtin_fmaf(v[e], weight[c], o[e]);
+    }
+    store8(&so[grp][d8], o);
+    __syncthreads();
+    if (grp)
+        return;
+    const int groups = min(GROUPS, chunks);
+    for (int k = 1; k < groups; ++k) {
+        float v[8];
+        load8(&so[k][d8], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            o[e] += v[e];
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
@@ -361,51 +344,76 @@ __global__ __launch_bounds__(256) void attn_join(const AttnArgs g)
     store8(static_cast<OT *>(a.out) + tok * a.ld_out + (int64_t)hq * D + d8, o);
 }
 
+// Pieces of the keys so that about `want` workgroups run, none of fewer than
+// `least` keys.
+static void split_keys(AttnSplit &s, const bq_attn &a, int64_t want, int64_t least)
+{
+    const int64_t group = a.q_heads / a.cache.heads;
+    // tiles that can have rows: no request has more than s.tiles, all together no more than the rows allow
+    const int64_t all = a.tokens * group / s.cols + a.requests, each = (int64_t)s.tiles * a.requests;
+    const int64_t busy = (each < all ? each : all) * a.cache.heads;
+    int64_t chunks = want / (busy < 1 ? 1 : busy);
+    const int64_t steps = (a.max_keys + least - 1) / least;
+    chunks = chunks > steps ? steps : chunks;
+    chunks = chunks > kMaxChunks ? kMaxChunks : chunks;
+    if (chunks < 1)
+        chunks = 1;
+    const int64_t per = steps < 1 ? 1 : (steps + chunks - 1) / chunks;
+    s.chunk = (int)(per * least);
+    s.chunks = (int)(steps < 1 ? 1 : (steps + per - 1) / per);
+}
+
 AttnPlan attn_plan(const bq_attn &a)
 {
     AttnPlan p;
     const int group = a.q_heads / a.cache.heads;
     const int64_t most = a.max_new < a.tokens ? a.max_new : a.tokens;
     const int64_t rows = most * group;
-    p.nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    p.tiles = (int)((rows + 16 * p.nt - 1) / (16 * p.nt));
-    // tiles that can have rows: no request has more than `tiles`, all together no more than the rows allow
-    const int64_t all = a.tokens * group / (16 * p.nt) + a.requests;
-    const int64_t busy = (p.tiles * (int64_t)a.requests < all ? p.tiles * (int64_t)a.requests : all) * a.cache.heads;
-    int64_t chunks = (1024 + busy - 1) / busy;
-    const int64_t step = kAttnKeys * kAttnWaves;
-    const int64_t steps = (a.max_keys + step - 1) / step;
-    chunks = chunks > steps ? steps : chunks;
-    chunks = chunks < 1 ? 1 : chunks > 64 ? 64 : chunks;
-    const int64_t each = (steps + chunks - 1) / chunks;
-    p.chunk = (int)((each < 1 ? 1 : each) * step);
-    p.chunks = (int)((steps + (each < 1 ? 1 : each) - 1) / (each < 1 ? 1 : each));
-    p.chunks = p.chunks < 1 ? 1 : p.chunks;
-    p.work_bytes = p.chunks > 1 ? a.tokens * a.q_heads * p.chunks * (4 * (int64_t)a.cache.dim + 8) : 0;
+    p.many.cols = p.many.tiles = p.many.chunk = 0;
+    p.many.chunks = 1;
+    p.few.cols = rows <= 16 || rows > kFewRows ? 16 : rows <= 32 ? 32 : 64;
+    p.few.tiles = (int)(((rows > kFewRows ? kFewRows : rows) + p.few.cols - 1) / p.few.cols);
+    split_keys(p.few, a, 2048, kAttnStep);
+    if (rows > kFewRows && a.requests == 1) {  // one request: one kernel
+        p.few.tiles = 0;
+        p.few.chunks = 1;
+    }
+    if (rows > kFewRows) {
+        p.many.cols = rows <= 128 || a.type == BQ_F32 ? 128 : 256;
+        const int64_t tiles = (rows + p.many.cols - 1) / p.many.cols;
+        p.many.tiles = (int)(tiles < 32768 ? tiles : 32768);  // a grid dimension; the kernel walks on from there
+        split_keys(p.many, a, 512, 512);
+    }
+    p.stride = p.few.chunks > p.many.chunks ? p.few.chunks : p.many.chunks;
+    p.work_bytes = p.stride > 1 ? a.tokens * a.q_heads * p.stride * (4 * (int64_t)a.cache.dim + 8) : 0;
     return p;
 }
 
 template <int CT, int D, bool F32>
 static void attn_nt(const AttnArgs &g, dim3 grid, hipStream_t st)
 {
-    switch (g.p.nt) {
-    case 1: hipLaunchKernelGGL((attn_kernel<CT, D, 1, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
-    case 2: hipLaunchKernelGGL((attn_kernel<CT, D, 2, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
+    switch (g.p.few.cols) {
+    case 16: hipLaunchKernelGGL((attn_kernel<CT, D, 1, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
+    case 32: hipLaunchKernelGGL((attn_kernel<CT, D, 2, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
     default: hipLaunchKernelGGL((attn_kernel<CT, D, 4, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
     }
 }
 
 template <int CT, int D>
-static void attn_dim(const AttnArgs &g, dim3 grid, dim3 join, hipStream_t st)
+static void attn_dim(const AttnArgs &g, dim3 grid, hipStream_t st)
 {
     const bool f32 = g.a.type == BQ_F32;
     f32 ? attn_nt<CT, D, true>(g, grid, st) : attn_nt<CT, D, false>(g, grid, st);
-    if (g.p.chunks > 1) {
-        if (f32)
-            hipLaunchKernelGGL((attn_join<float, D>), join, dim3(256), 0, st, g);
-        else
-            hipLaunchKernelGGL((attn_join<typename Num<CT>::t, D>), join, dim3(256), 0, st, g);
-    }
+}
+
+template <int CT, int D>
+static void join_dim(const AttnArgs &g, hipStream_t st)
+{
+    const dim3 grid((unsigned)(g.a.tokens * g.a.q_heads));
+    if (g.a.type == BQ_F32)
+        hipLaunchKernelGGL((attn_join<float, D>), grid, dim3(256), 0, st, g);
+    else
+        hipLaunchKernelGGL((attn_join<typename Num<CT>::t, D>), grid, dim3(256), 0, st, g);
 }
 
 hipError_t launch_attn(const bq_attn &a, const AttnPlan &p, hipStream_t st)
@@ -415,12 +423,25 @@ hipError_t launch_attn(const bq_attn &a, const AttnPlan &p, hipStream_t st)
     g.p = p;
     g.group = a.q_heads / a.cache.heads;
     g.page_log2 = __builtin_ctz((unsigned)a.cache.page);
-    const dim3 grid((unsigned)(p.tiles * p.chunks), (unsigned)a.cache.heads, (unsigned)a.requests);
-    const dim3 join((unsigned)((a.tokens * a.q_heads * (a.cache.dim / 8) + 255) / 256));
-    if (a.cache.type == BQ_F16)
-        a.cache.dim == 64 ? attn_dim<BQ_F16, 64>(g, grid, join, st) : attn_dim<BQ_F16, 128>(g, grid, join, st);
-    else
-        a.cache.dim == 64 ? attn_dim<BQ_BF16, 64>(g, grid, join, st) : attn_dim<BQ_BF16, 128>(g, grid, join, st);
+    const bool wide = a.cache.dim == 128, f16 = a.cache.type == BQ_F16;
+    if (p.many.tiles) {
+        const hipError_t e = launch_attn_tiles(g, st);
+        if (e != hipSuccess)
+            return e;
+    }
+    if (p.few.tiles) {
+        const dim3 grid((unsigned)a.cache.heads, (unsigned)(p.few.tiles * p.few.chunks), (unsigned)a.requests);
+        if (f16)
+            wide ? attn_dim<BQ_F16, 128>(g, grid, st) : attn_dim<BQ_F16, 64>(g, grid, st);
+        else
+            wide ? attn_dim<BQ_BF16, 128>(g, grid, st) : attn_dim<BQ_BF16, 64>(g, grid, st);
+    }
+    if (p.stride > 1) {
+        if (f16)
+            wide ? join_dim<BQ_F16, 128>(g, st) : join_dim<BQ_F16, 64>(g, st);
+        else
+            wide ? join_dim<BQ_BF16, 128>(g, st) : join_dim<BQ_BF16, 64>(g, st);
+    }
     return hipGetLastError();
 }
 

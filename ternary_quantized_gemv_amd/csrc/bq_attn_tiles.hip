@@ -1,0 +1,299 @@
+// bq_attn_tiles.hip -- attention of many new tokens (whole prompts, long
+// chunks) over the paged cache: the arithmetic of bq_attn.hip with the keys
+// shared through LDS.
+//
+// A workgroup of four wavefronts takes 128 NC rows (G query heads of each
+// token) of one key head, 32 NC columns a wavefront, and 64 keys at a time.
+// The products are v_mfma_f32_32x32x16, again S^T = K Q^T and O^T = V^T P^T:
+// result register r of lane l holds row 8 (r / 4) + 4 (l / 32) + r % 4 of column
+// l % 32, and operands hold k = 8 (l / 32) + e.  Row 8 a + 4 h + i of a 32-key
+// tile is assigned key 16 (a / 2) + 8 h + 4 (a % 2) + i, so that a lane's
+// registers 8 s .. 8 s + 7 are keys 16 s + 8 h .. + 7: the B operand of the
+// second product as they stand.  Both tiles lie in LDS in 16-byte pieces, piece
+// c of row r at c ^ (r % 8) of the row, so that the eight lanes that a read
+// serves at a time touch all banks once.
+//
+// The running maximum is only raised when a tile's exceeds it by 2^8: until
+// then the weights are at most 2^8 times larger than they would be, which
+// changes no relative error, and the D sums of a column are not rescaled.
+// (f16 weights are scaled by 2^6, which leaves room for that below 2^16.)
+//
+// The matrix cores bound it: 4 D operations per row and key against 4 D / (128
+// NC) bytes of LDS and less of memory.
+#include "bq_attn.h"
+
+namespace bq {
+
+constexpr int kTileKeys = 64;
+constexpr float kSlack = 8.0f;  // log2
+
+template <int CT, int D, int NC, bool F32>
+__global__ __launch_bounds__(256, 1) void attn_tiles(const AttnArgs g)
+{
+    typedef typename Num<CT>::t T;
+    typedef typename Num<CT>::v8 v8;
+    constexpr int NP = F32 ? Parts<T>::n : 1;
+    constexpr float UP = CT == BQ_F16 ? 6.0f : 0.0f;
+    constexpr int DJ = D / 16, DT = D / 32, KC = D / 8;   // steps and tiles of D; 16-byte pieces of a key
+    constexpr int KL = kTileKeys * KC / 256, VL = D * 8 / 256;  // pieces a thread stages
+    __shared__ v8 ks[2][kTileKeys * KC];
+    __shared__ v8 vs[2][D * 8];
+
+    const bq_attn &a = g.a;
+    const AttnSplit &sp = g.p.many;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c32 = lane & 31, half = lane >> 5;
+    const int b = blockIdx.z, kh = blockIdx.x;
+    const Request rq = request_at(a, b);
+    const int64_t rows64 = (int64_t)rq.n * g.group;
+    if (rq.n <= 0 || has_few(g.p, (int)rows64))
+        return;
+    const int rows = (int)rows64;
+    // the last tile first: it sees the most keys
+    const int tiles = (rows + 128 * NC - 1) / (128 * NC);
+    const int turn = blockIdx.y / sp.chunks, chunk = blockIdx.y % sp.chunks;
+    const int P = a.cache.page, pmask = P - 1;
+    const int64_t page_elems = ((int64_t)a.cache.heads << g.page_log2) * D;
+    const T *kbase = static_cast<const T *>(a.cache.k) + (int64_t)kh * P * D;
+    const T *vbase = static_cast<const T *>(a.cache.v) + (int64_t)kh * D * P;
+    const int32_t *table = a.table + (int64_t)b * a.ld_table;
+
+    // staging: piece tid + 256 i of a tile.  K row r, piece c holds key order(r)'s values 8 c .. 8 c + 7
+    const int kc = threadIdx.x % KC, kr = threadIdx.x / KC;
+    const int vc = threadIdx.x % 8, vr = threadIdx.x / 8;
+
+    for (int u = turn; u < tiles; u += sp.tiles) {
+        const int r0 = (tiles - 1 - u) * 128 * NC;
+        const int w0 = r0 + wave * 32 * NC;
+        v8 qf[NC][NP][DJ];
+        float qs[NC], m[NC], l[NC];
+        int last[NC];
+#pragma unroll
+        for (int t = 0; t < NC; ++t) {
+            const int r = w0 + 32 * t + c32;
+            const bool live = r < rows;
+            const int i = live ? r / g.group : 0, hq = kh * g.group + (live ? r % g.group : 0);
+            last[t] = live ? rq.keys - rq.n + i : -1;
+            m[t] = kNone;
+            l[t] = 0.0f;
+            qs[t] = load_query<T, v8, NP, DJ, F32>(a, (int64_t)(rq.row0 + i) * a.ld_q + (int64_t)hq * D + 8 * half, 16, qf[t],
+                                                   [](float x) { return fmaxf(x, __shfl_xor(x, 32, 64)); });
+        }
+        f32x16 o[NC][DT];
+#pragma unroll
+        for (int t = 0; t < NC; ++t)
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    o[t][d][r] = 0.0f;
+
+        const int last_row = min(r0 + 128 * NC, rows) - 1;
+        const int seen = min(rq.keys, rq.keys - rq.n + last_row / g.group + 1);
+        const int begin = chunk * sp.chunk;
+        const int end = chunk == sp.chunks - 1 ? seen : min(seen, begin + sp.chunk);
+        const int first_last = rq.keys - rq.n + r0 / g.group;
+
+        // ---- staging of one tile: memory to registers, registers to LDS
+        v8 kreg[KL], vreg[VL];
+        int vpage = -1;
+        bool bad = false;  // a piece of the tile has no page
+        auto fetch = [&](int k0) {
+            bad = false;
+#pragma unroll
+            for (int i = 0; i < KL; ++i) {
+                const int r = kr + i * (256 / KC), ri = r & 31;
+                // row 8 a + 4 h + i of 32 is key 16 (a / 2) + 8 h + 4 (a % 2) + i
+                const int key = k0 + (r & 32) + 16 * (ri >> 4) + 8 * ((ri >> 2) & 1) + 4 * ((ri >> 3) & 1) + (ri & 3);
+                const int page = page_at(g, table, key, end);
+                bad |= page < 0;
+                kreg[i] = *reinterpret_cast<const v8 *>(kbase + (int64_t)max(page, 0) * page_elems + (key & pmask) * D + 8 * kc);
+            }
+            const int key = k0 + 8 * vc;
+            vpage = page_at(g, table, key, end);
+            const T *p = vbase + (int64_t)max(vpage, 0) * page_elems + (key & pmask);
+#pragma unroll
+            for (int i = 0; i < VL; ++i)
+                vreg[i] = *reinterpret_cast<const v8 *>(p + (vr + 32 * i) * P);
+        };
+        auto stage = [&](int k0, int buf) {
+#pragma unroll
+            for (int i = 0; i < KL; ++i) {
+                const int r = kr + i * (256 / KC);
+                ks[buf][r * KC + (kc ^ (r & 7))] = kreg[i];
+            }
+            if (k0 + kTileKeys > end || vpage < 0) {
+                // places that no row sees may hold anything: their values must not meet a weight of 0
+#pragma unroll
+                for (int i = 0; i < VL; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        vreg[i][e] = k0 + 8 * vc + e < end && vpage >= 0 ? vreg[i][e] : (T)0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < VL; ++i) {
+                const int r = vr + 32 * i;
+                vs[buf][r * 8 + (vc ^ (r & 7))] = vreg[i];
+            }
+        };
+
+        int buf = 0;
+        bool holes = false;
+        if (begin < end) {
+            fetch(begin);
+            stage(begin, 0);
+            holes = __syncthreads_or(bad);
+        }
+        for (int k0 = begin; k0 < end; k0 += kTileKeys) {
+            const int next = k0 + kTileKeys;
+            if (next < end)
+                fetch(next);
+            const bool whole = k0 + kTileKeys - 1 <= first_last && k0 + kTileKeys <= end && !holes;
+            // ---- scores
+            f32x16 s[NC][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int t = 0; t < NC; ++t)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        s[t][h][r] = 0.0f;
+                const int row = 32 * h + c32;
+#pragma unroll
+                for (int j = 0; j < DJ; ++j) {
+                    const v8 kf = ks[buf][row * KC + ((2 * j + half) ^ (row & 7))];
+#pragma unroll
+                    for (int t = 0; t < NC; ++t)
+#pragma unroll
+                        for (int p = NP - 1; p >= 0; --p)
+                            s[t][h] = Num<CT>::mfma32(kf, qf[t][p][j], s[t][h]);
+                }
+            }
+            // ---- weights
+            v8 pf[NC][NP][4];
+#pragma unroll
+            for (int t = 0; t < NC; ++t) {
+                float factor = qs[t], top = kNone;
+                if (!whole) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const int key = k0 + 32 * h + 16 * (r >> 3) + 8 * half + (r & 7);
+                            const bool sees = key <= last[t] && key < end && (!holes || page_at(g, table, key, end) >= 0);
+                            s[t][h][r] = sees ? s[t][h][r] * factor : kNone;
+                        }
+                    factor = 1.0f;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        top = fmaxf(top, s[t][h][r]);
+                top = fmaxf(top, __shfl_xor(top, 32, 64)) * factor;
+                if (__any(top > m[t] + kSlack)) {
+                    const float mn = fmaxf(m[t], top);
+                    const float f = __builtin_amdgcn_exp2f(m[t] - (mn == kNone ? 0.0f : mn));
+                    m[t] = mn;
+                    l[t] *= f;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+                        o[t][d] *= f;
+                }
+                const float shift = UP - (m[t] == kNone ? 0.0f : m[t]);
+                float sum = 0.0f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        float rest = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][h][r], factor, shift));
+                        sum += rest;
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) {
+                            pf[t][p][2 * h + (r >> 3)][r & 7] = (T)rest;
+                            rest -= (float)pf[t][p][2 * h + (r >> 3)][r & 7];
+                        }
+                    }
+                l[t] += sum;
+            }
+            // ---- values
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const int row = 32 * d + c32;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const v8 vf = vs[buf][row * 8 + ((2 * k + half) ^ (row & 7))];
+#pragma unroll
+                    for (int t = 0; t < NC; ++t)
+#pragma unroll
+                        for (int p = NP - 1; p >= 0; --p)
+                            o[t][d] = Num<CT>::mfma32(vf, pf[t][p][k], o[t][d]);
+                }
+            }
+            if (next < end)
+                stage(next, buf ^ 1);
+            holes = __syncthreads_or(next < end && bad);
+            buf ^= 1;
+        }
+        // ---- out, or this chunk's part of it
+#pragma unroll
+        for (int t = 0; t < NC; ++t) {
+            l[t] += __shfl_xor(l[t], 32, 64);
+            const int r = w0 + 32 * t + c32;
+            if (r >= rows)
+                continue;
+            const int64_t tok = rq.row0 + r / g.group;
+            const int hq = kh * g.group + r % g.group;
+            const int64_t row = tok * a.q_heads + hq;
+            const float f = sp.chunks > 1 ? 1.0f : l[t] > 0.0f ? 1.0f / l[t] : 0.0f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int at = 32 * d + 8 * q + 4 * half;
+                    f32x4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = o[t][d][4 * q + e] * f;
+                    if (sp.chunks > 1) {
+                        *reinterpret_cast<f32x4 *>(part_sums(g, row, chunk, D) + at) = v;
+                    } else if constexpr (F32) {
+                        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + tok * a.ld_out + (int64_t)hq * D + at) = v;
+                    } else {
+                        typedef T tx4 __attribute__((ext_vector_type(4)));
+                        tx4 x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[e] = (T)v[e];
+                        *reinterpret_cast<tx4 *>(static_cast<T *>(a.out) + tok * a.ld_out + (int64_t)hq * D + at) = x;
+                    }
+                }
+            if (sp.chunks > 1 && half == 0)
+                *part_stats(g, row, chunk, D) = make_float2(m[t], l[t]);
+        }
+    }
+}
+
+template <int CT, int D>
+static void tiles_dim(const AttnArgs &g, dim3 grid, hipStream_t st)
+{
+    if (g.a.type == BQ_F32)
+        hipLaunchKernelGGL((attn_tiles<CT, D, 1, true>), grid, dim3(256), 0, st, g);
+    else if (g.p.many.cols == 128)
+        hipLaunchKernelGGL((attn_tiles<CT, D, 1, false>), grid, dim3(256), 0, st, g);
+    else
+        hipLaunchKernelGGL((attn_tiles<CT, D, 2, false>), grid, dim3(256), 0, st, g);
+}
+
+hipError_t launch_attn_tiles(const AttnArgs &g, hipStream_t st)
+{
+    const bq_attn &a = g.a;
+    const dim3 grid((unsigned)a.cache.heads, (unsigned)(g.p.many.tiles * g.p.many.chunks), (unsigned)a.requests);
+    if (a.cache.type == BQ_F16)
+        a.cache.dim == 64 ? tiles_dim<BQ_F16, 64>(g, grid, st) : tiles_dim<BQ_F16, 128>(g, grid, st);
+    else
+        a.cache.dim == 64 ? tiles_dim<BQ_BF16, 64>(g, grid, st) : tiles_dim<BQ_BF16, 128>(g, grid, st);
+    return hipGetLastError();
+}
+
+}  // namespace bq

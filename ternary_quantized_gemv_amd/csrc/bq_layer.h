@@ -23,14 +23,19 @@ hipError_t launch_norm(int type, const NormArgs &a, int64_t rows, hipStream_t st
 
 hipError_t launch_append(const bq_append &a, hipStream_t st);
 
-// How bq_paged_attn splits its work (attn_plan): tiles of 16 nt rows of one
-// key head's queries, `tiles` of them at most per request, each over `chunks`
-// pieces of `chunk` keys that the join adds up.
-struct AttnPlan {
-    int nt;
+// How bq_paged_attn splits its work (attn_plan), for each of its two kernels:
+// tiles of `cols` rows of one key head's queries, `tiles` of them at most per
+// request (0: not launched), each over `chunks` pieces of `chunk` keys that the
+// join adds up.
+struct AttnSplit {
+    int cols;
     int tiles;
     int chunks;
     int chunk;
+};
+struct AttnPlan {
+    AttnSplit few, many;
+    int stride;  // places per row for the pieces
     int64_t work_bytes;
 };
 AttnPlan attn_plan(const bq_attn &a);
