@@ -75,10 +75,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
             m[t] = kNone;
             l[t] = 0.0f;
             qs[t] = load_query<T, v8, NP, DJ, F32>(a, (int64_t)(rq.row0 + i) * a.ld_q + (int64_t)hq * D + 8 * q4, 32, qf[t],
-                                                   [](float x) {
-                                                       x = fmaxf(x, __shfl_xor(x, 16, 64));
-                                                       return fmaxf(x, __shfl_xor(x, 32, 64));
-                                                   });
+                                                   [](float x) { return across32(across16(x, Max()), Max()); });
         }
         f32x4 o[NT][DT];
 #pragma unroll
@@ -159,8 +156,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     top = fmaxf(top, w[e]);
-                top = fmaxf(top, __shfl_xor(top, 16, 64));
-                top = fmaxf(top, __shfl_xor(top, 32, 64)) * factor;
+                top = across32(across16(top, Max()), Max()) * factor;
                 if (__any(top > m[t])) {
                     const float mn = fmaxf(m[t], top);
                     const float f = __builtin_amdgcn_exp2f(m[t] - (mn == kNone ? 0.0f : mn));
@@ -198,8 +194,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
         // ---- the four wavefronts' sums become one; l over the lane's key groups first
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            l[t] += __shfl_xor(l[t], 16, 64);
-            l[t] += __shfl_xor(l[t], 32, 64);
+            l[t] = across32(across16(l[t], Add()), Add());
             if (q4 == 0) {
                 sm[wave][t][c16] = m[t];
                 sl[wave][t][c16] = l[t];

@@ -2,8 +2,8 @@
 // chunks) over the paged cache: the arithmetic of bq_attn.hip with the keys
 // shared through LDS.
 //
-// A workgroup of four wavefronts takes 128 NC rows (G query heads of each
-// token) of one key head, 32 NC columns a wavefront, and 64 keys at a time.
+// A workgroup of four or eight wavefronts takes 128 or 256 rows (G query heads
+// of each token) of one key head, 32 columns a wavefront, and 64 keys at a time.
 // The products are v_mfma_f32_32x32x16, again S^T = K Q^T and O^T = V^T P^T:
 // result register r of lane l holds row 8 (r / 4) + 4 (l / 32) + r % 4 of column
 // l % 32, and operands hold k = 8 (l / 32) + e.  Row 8 a + 4 h + i of a 32-key
@@ -27,15 +27,19 @@ namespace bq {
 constexpr int kTileKeys = 64;
 constexpr float kSlack = 8.0f;  // log2
 
-template <int CT, int D, int NC, bool F32>
-__global__ __launch_bounds__(256, 1) void attn_tiles(const AttnArgs g)
+template <int CT, int D, int WAVES, bool F32>
+__global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnArgs g)
 {
     typedef typename Num<CT>::t T;
     typedef typename Num<CT>::v8 v8;
     constexpr int NP = F32 ? Parts<T>::n : 1;
     constexpr float UP = CT == BQ_F16 ? 6.0f : 0.0f;
-    constexpr int DJ = D / 16, DT = D / 32, KC = D / 8;   // steps and tiles of D; 16-byte pieces of a key
-    constexpr int KL = kTileKeys * KC / 256, VL = D * 8 / 256;  // pieces a thread stages
+    constexpr int THREADS = 64 * WAVES, ROWS = 32 * WAVES;
+    constexpr int DJ = D / 16, DT = D / 32, KC = D / 8;  // steps and tiles of D; 16-byte pieces of a key
+    constexpr int BLOCKS = kTileKeys / 16;               // of 16 keys: one page each
+    constexpr int KL = kTileKeys * KC / THREADS, VL = D * 8 / THREADS;  // pieces a thread stages
+    constexpr int KROWS = THREADS / KC, VROWS = THREADS / 8;            // rows that one piece of each thread covers
+    static_assert(KROWS % 16 == 0 && KL >= 1 && VL >= 1, "a thread's piece of keys stays in one 16-key block per 16 rows");
     __shared__ v8 ks[2][kTileKeys * KC];
     __shared__ v8 vs[2][D * 8];
 
@@ -50,7 +54,7 @@ __global__ __launch_bounds__(256, 1) void attn_tiles(const AttnArgs g)
         return;
     const int rows = (int)rows64;
     // the last tile first: it sees the most keys
-    const int tiles = (rows + 128 * NC - 1) / (128 * NC);
+    const int tiles = (rows + ROWS - 1) / ROWS;
     const int turn = blockIdx.y / sp.chunks, chunk = blockIdx.y % sp.chunks;
     const int P = a.cache.page, pmask = P - 1;
     const int64_t page_elems = ((int64_t)a.cache.heads << g.page_log2) * D;
@@ -58,71 +62,77 @@ __global__ __launch_bounds__(256, 1) void attn_tiles(const AttnArgs g)
     const T *vbase = static_cast<const T *>(a.cache.v) + (int64_t)kh * D * P;
     const int32_t *table = a.table + (int64_t)b * a.ld_table;
 
-    // staging: piece tid + 256 i of a tile.  K row r, piece c holds key order(r)'s values 8 c .. 8 c + 7
+    // staging: a thread's pieces are piece kc of rows kr + KROWS i (keys) and piece vc of rows vr + VROWS i (values)
     const int kc = threadIdx.x % KC, kr = threadIdx.x / KC;
     const int vc = threadIdx.x % 8, vr = threadIdx.x / 8;
 
     for (int u = turn; u < tiles; u += sp.tiles) {
-        const int r0 = (tiles - 1 - u) * 128 * NC;
-        const int w0 = r0 + wave * 32 * NC;
-        v8 qf[NC][NP][DJ];
-        float qs[NC], m[NC], l[NC];
-        int last[NC];
+        const int r0 = (tiles - 1 - u) * ROWS;
+        const int r = r0 + wave * 32 + c32;
+        const bool live = r < rows;
+        const int i_tok = live ? r / g.group : 0, hq = kh * g.group + (live ? r % g.group : 0);
+        const int last = live ? rq.keys - rq.n + i_tok : -1;
+        float m = kNone, l = 0.0f;
+        v8 qf[NP][DJ];
+        const float qs = load_query<T, v8, NP, DJ, F32>(a, (int64_t)(rq.row0 + i_tok) * a.ld_q + (int64_t)hq * D + 8 * half, 16,
+                                                        qf, [](float x) { return across32(x, Max()); });
+        f32x16 o[DT];
 #pragma unroll
-        for (int t = 0; t < NC; ++t) {
-            const int r = w0 + 32 * t + c32;
-            const bool live = r < rows;
-            const int i = live ? r / g.group : 0, hq = kh * g.group + (live ? r % g.group : 0);
-            last[t] = live ? rq.keys - rq.n + i : -1;
-            m[t] = kNone;
-            l[t] = 0.0f;
-            qs[t] = load_query<T, v8, NP, DJ, F32>(a, (int64_t)(rq.row0 + i) * a.ld_q + (int64_t)hq * D + 8 * half, 16, qf[t],
-                                                   [](float x) { return fmaxf(x, __shfl_xor(x, 32, 64)); });
-        }
-        f32x16 o[NC][DT];
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int t = 0; t < NC; ++t)
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    o[t][d][r] = 0.0f;
+            for (int e = 0; e < 16; ++e)
+                o[d][e] = 0.0f;
 
-        const int last_row = min(r0 + 128 * NC, rows) - 1;
+        const int last_row = min(r0 + ROWS, rows) - 1;
         const int seen = min(rq.keys, rq.keys - rq.n + last_row / g.group + 1);
         const int begin = chunk * sp.chunk;
         const int end = chunk == sp.chunks - 1 ? seen : min(seen, begin + sp.chunk);
         const int first_last = rq.keys - rq.n + r0 / g.group;
 
-        // ---- staging of one tile: memory to registers, registers to LDS
+        // ---- staging of one tile: pages (one tile ahead), memory to registers, registers to LDS
         v8 kreg[KL], vreg[VL];
+        int page[BLOCKS];
+        auto look_up = [&](int k0) {
+#pragma unroll
+            for (int i = 0; i < BLOCKS; ++i) {
+                const int key = k0 + 16 * i;
+                const int p = key < end ? uniform_word(table + (key >> g.page_log2)) : -1;
+                page[i] = (unsigned)p < (unsigned)a.cache.pages ? p : -1;
+            }
+        };
+        bool holes = false, bad = false;  // a page of this (the next) tile is outside the cache, or it ends early
         int vpage = -1;
-        bool bad = false;  // a piece of the tile has no page
         auto fetch = [&](int k0) {
             bad = false;
 #pragma unroll
+            for (int i = 0; i < BLOCKS; ++i)
+                bad |= page[i] < 0;
+#pragma unroll
             for (int i = 0; i < KL; ++i) {
-                const int r = kr + i * (256 / KC), ri = r & 31;
+                const int row = kr + KROWS * i, ri = row & 31;
                 // row 8 a + 4 h + i of 32 is key 16 (a / 2) + 8 h + 4 (a % 2) + i
-                const int key = k0 + (r & 32) + 16 * (ri >> 4) + 8 * ((ri >> 2) & 1) + 4 * ((ri >> 3) & 1) + (ri & 3);
-                const int page = page_at(g, table, key, end);
-                bad |= page < 0;
-                kreg[i] = *reinterpret_cast<const v8 *>(kbase + (int64_t)max(page, 0) * page_elems + (key & pmask) * D + 8 * kc);
+                const int key = k0 + (row & ~15) + 8 * ((ri >> 2) & 1) + 4 * ((ri >> 3) & 1) + (ri & 3);
+                int p;
+                if constexpr (KROWS == 16)
+                    p = page[i];
+                else  // the thread's 16-key block of KROWS / 16 neighbours
+                    p = kr < 16 ? page[i * (KROWS / 16)] : KROWS == 32 || kr < 32 ? page[i * (KROWS / 16) + 1]
+                        : kr < 48 ? page[(i * (KROWS / 16) + 2) % BLOCKS] : page[(i * (KROWS / 16) + 3) % BLOCKS];
+                kreg[i] = *reinterpret_cast<const v8 *>(kbase + (int64_t)max(p, 0) * page_elems + (key & pmask) * D + 8 * kc);
             }
-            const int key = k0 + 8 * vc;
-            vpage = page_at(g, table, key, end);
-            const T *p = vbase + (int64_t)max(vpage, 0) * page_elems + (key & pmask);
+            vpage = vc < 2 ? page[0] : vc < 4 ? page[1] : vc < 6 ? page[2] : page[3];
+            const T *p = vbase + (int64_t)max(vpage, 0) * page_elems + ((k0 + 8 * vc) & pmask);
 #pragma unroll
             for (int i = 0; i < VL; ++i)
-                vreg[i] = *reinterpret_cast<const v8 *>(p + (vr + 32 * i) * P);
+                vreg[i] = *reinterpret_cast<const v8 *>(p + (vr + VROWS * i) * P);
         };
         auto stage = [&](int k0, int buf) {
 #pragma unroll
             for (int i = 0; i < KL; ++i) {
-                const int r = kr + i * (256 / KC);
-                ks[buf][r * KC + (kc ^ (r & 7))] = kreg[i];
+                const int row = kr + KROWS * i;
+                ks[buf][row * KC + (kc ^ (row & 7))] = kreg[i];
             }
-            if (k0 + kTileKeys > end || vpage < 0) {
+            if (k0 + kTileKeys > end || bad) {
                 // places that no row sees may hold anything: their values must not meet a weight of 0
 #pragma unroll
                 for (int i = 0; i < VL; ++i)
@@ -132,145 +142,130 @@ __global__ __launch_bounds__(256, 1) void attn_tiles(const AttnArgs g)
             }
 #pragma unroll
             for (int i = 0; i < VL; ++i) {
-                const int r = vr + 32 * i;
-                vs[buf][r * 8 + (vc ^ (r & 7))] = vreg[i];
+                const int row = vr + VROWS * i;
+                vs[buf][row * 8 + (vc ^ (row & 7))] = vreg[i];
             }
         };
 
         int buf = 0;
-        bool holes = false;
         if (begin < end) {
+            look_up(begin);
             fetch(begin);
+            look_up(begin + kTileKeys);
             stage(begin, 0);
-            holes = __syncthreads_or(bad);
+            holes = bad;
+            __syncthreads();
         }
         for (int k0 = begin; k0 < end; k0 += kTileKeys) {
             const int next = k0 + kTileKeys;
-            if (next < end)
+            if (next < end) {
                 fetch(next);
+                look_up(next + kTileKeys);
+            }
             const bool whole = k0 + kTileKeys - 1 <= first_last && k0 + kTileKeys <= end && !holes;
-            // ---- scores
-            f32x16 s[NC][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                // ---- scores
+                f32x16 s;
 #pragma unroll
-                for (int t = 0; t < NC; ++t)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        s[t][h][r] = 0.0f;
-                const int row = 32 * h + c32;
+                for (int e = 0; e < 16; ++e)
+                    s[e] = 0.0f;
+                const int krow = 32 * h + c32;
 #pragma unroll
                 for (int j = 0; j < DJ; ++j) {
-                    const v8 kf = ks[buf][row * KC + ((2 * j + half) ^ (row & 7))];
+                    const v8 kf = ks[buf][krow * KC + ((2 * j + half) ^ (krow & 7))];
 #pragma unroll
-                    for (int t = 0; t < NC; ++t)
-#pragma unroll
-                        for (int p = NP - 1; p >= 0; --p)
-                            s[t][h] = Num<CT>::mfma32(kf, qf[t][p][j], s[t][h]);
+                    for (int p = NP - 1; p >= 0; --p)
+                        s = Num<CT>::mfma32(kf, qf[p][j], s);
                 }
-            }
-            // ---- weights
-            v8 pf[NC][NP][4];
-#pragma unroll
-            for (int t = 0; t < NC; ++t) {
-                float factor = qs[t], top = kNone;
+                // ---- weights
+                float factor = qs, top = kNone;
                 if (!whole) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const int key = k0 + 32 * h + 16 * (r >> 3) + 8 * half + (r & 7);
-                            const bool sees = key <= last[t] && key < end && (!holes || page_at(g, table, key, end) >= 0);
-                            s[t][h][r] = sees ? s[t][h][r] * factor : kNone;
-                        }
+                    for (int e = 0; e < 16; ++e) {
+                        const int key = k0 + 32 * h + 16 * (e >> 3) + 8 * half + (e & 7);
+                        const bool sees = key <= last && key < end && (!holes || page_at(g, table, key, end) >= 0);
+                        s[e] = sees ? s[e] * factor : kNone;
+                    }
                     factor = 1.0f;
                 }
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        top = fmaxf(top, s[t][h][r]);
-                top = fmaxf(top, __shfl_xor(top, 32, 64)) * factor;
-                if (__any(top > m[t] + kSlack)) {
-                    const float mn = fmaxf(m[t], top);
-                    const float f = __builtin_amdgcn_exp2f(m[t] - (mn == kNone ? 0.0f : mn));
-                    m[t] = mn;
-                    l[t] *= f;
+                for (int e = 0; e < 16; ++e)
+                    top = fmaxf(top, s[e]);
+                top = across32(top, Max()) * factor;
+                if (__any(top > m + kSlack)) {
+                    const float mn = fmaxf(m, top);
+                    const float f = __builtin_amdgcn_exp2f(m - (mn == kNone ? 0.0f : mn));
+                    m = mn;
+                    l *= f;
 #pragma unroll
                     for (int d = 0; d < DT; ++d)
-                        o[t][d] *= f;
+                        o[d] *= f;
                 }
-                const float shift = UP - (m[t] == kNone ? 0.0f : m[t]);
+                const float shift = UP - (m == kNone ? 0.0f : m);
                 float sum = 0.0f;
+                v8 pf[NP][2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int e = 0; e < 16; ++e) {
+                    float rest = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], factor, shift));
+                    sum += rest;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        float rest = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][h][r], factor, shift));
-                        sum += rest;
-#pragma unroll
-                        for (int p = 0; p < NP; ++p) {
-                            pf[t][p][2 * h + (r >> 3)][r & 7] = (T)rest;
-                            rest -= (float)pf[t][p][2 * h + (r >> 3)][r & 7];
-                        }
+                    for (int p = 0; p < NP; ++p) {
+                        pf[p][e >> 3][e & 7] = (T)rest;
+                        rest -= (float)pf[p][e >> 3][e & 7];
                     }
-                l[t] += sum;
-            }
-            // ---- values
+                }
+                l += sum;
+                // ---- values
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const int row = 32 * d + c32;
+                for (int d = 0; d < DT; ++d) {
+                    const int row = 32 * d + c32;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const v8 vf = vs[buf][row * 8 + ((2 * k + half) ^ (row & 7))];
-#pragma unroll
-                    for (int t = 0; t < NC; ++t)
+                    for (int k = 0; k < 2; ++k) {
+                        const v8 vf = vs[buf][row * 8 + ((4 * h + 2 * k + half) ^ (row & 7))];
 #pragma unroll
                         for (int p = NP - 1; p >= 0; --p)
-                            o[t][d] = Num<CT>::mfma32(vf, pf[t][p][k], o[t][d]);
+                            o[d] = Num<CT>::mfma32(vf, pf[p][k], o[d]);
+                    }
                 }
             }
-            if (next < end)
+            if (next < end) {
                 stage(next, buf ^ 1);
-            holes = __syncthreads_or(next < end && bad);
+                holes = bad;
+            }
+            __syncthreads();
             buf ^= 1;
         }
         // ---- out, or this chunk's part of it
+        l = across32(l, Add());
+        if (!live)
+            continue;
+        const int64_t tok = rq.row0 + i_tok, row = tok * a.q_heads + hq;
+        const float f = sp.chunks > 1 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
-        for (int t = 0; t < NC; ++t) {
-            l[t] += __shfl_xor(l[t], 32, 64);
-            const int r = w0 + 32 * t + c32;
-            if (r >= rows)
-                continue;
-            const int64_t tok = rq.row0 + r / g.group;
-            const int hq = kh * g.group + r % g.group;
-            const int64_t row = tok * a.q_heads + hq;
-            const float f = sp.chunks > 1 ? 1.0f : l[t] > 0.0f ? 1.0f / l[t] : 0.0f;
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
+            for (int q = 0; q < 4; ++q) {
+                const int at = 32 * d + 8 * q + 4 * half;
+                f32x4 v;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int at = 32 * d + 8 * q + 4 * half;
-                    f32x4 v;
+                for (int e = 0; e < 4; ++e)
+                    v[e] = o[d][4 * q + e] * f;
+                if (sp.chunks > 1) {
+                    *reinterpret_cast<f32x4 *>(part_sums(g, row, chunk, D) + at) = v;
+                } else if constexpr (F32) {
+                    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + tok * a.ld_out + (int64_t)hq * D + at) = v;
+                } else {
+                    typedef T tx4 __attribute__((ext_vector_type(4)));
+                    tx4 x;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        v[e] = o[t][d][4 * q + e] * f;
-                    if (sp.chunks > 1) {
-                        *reinterpret_cast<f32x4 *>(part_sums(g, row, chunk, D) + at) = v;
-                    } else if constexpr (F32) {
-                        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + tok * a.ld_out + (int64_t)hq * D + at) = v;
-                    } else {
-                        typedef T tx4 __attribute__((ext_vector_type(4)));
-                        tx4 x;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[e] = (T)v[e];
-                        *reinterpret_cast<tx4 *>(static_cast<T *>(a.out) + tok * a.ld_out + (int64_t)hq * D + at) = x;
-                    }
+                        x[e] = (T)v[e];
+                    *reinterpret_cast<tx4 *>(static_cast<T *>(a.out) + tok * a.ld_out + (int64_t)hq * D + at) = x;
                 }
-            if (sp.chunks > 1 && half == 0)
-                *part_stats(g, row, chunk, D) = make_float2(m[t], l[t]);
-        }
+            }
+        if (sp.chunks > 1 && half == 0)
+            *part_stats(g, row, chunk, D) = make_float2(m, l);
     }
 }
 
@@ -278,11 +273,11 @@ template <int CT, int D>
 static void tiles_dim(const AttnArgs &g, dim3 grid, hipStream_t st)
 {
     if (g.a.type == BQ_F32)
-        hipLaunchKernelGGL((attn_tiles<CT, D, 1, true>), grid, dim3(256), 0, st, g);
+        hipLaunchKernelGGL((attn_tiles<CT, D, 4, true>), grid, dim3(256), 0, st, g);
     else if (g.p.many.cols == 128)
-        hipLaunchKernelGGL((attn_tiles<CT, D, 1, false>), grid, dim3(256), 0, st, g);
+        hipLaunchKernelGGL((attn_tiles<CT, D, 4, false>), grid, dim3(256), 0, st, g);
     else
-        hipLaunchKernelGGL((attn_tiles<CT, D, 2, false>), grid, dim3(256), 0, st, g);
+        hipLaunchKernelGGL((attn_tiles<CT, D, 8, false>), grid, dim3(512), 0, st, g);
 }
 
 hipError_t launch_attn_tiles(const AttnArgs &g, hipStream_t st)

@@ -89,6 +89,35 @@ __device__ __forceinline__ void store8(T *p, const float (&v)[8])
     }
 }
 
+// The maximum (or sum) over the two halves of a wavefront, and over the pairs
+// of 16-lane rows: lanes l, l ^ 32 and l, l ^ 16.
+template <class OP>
+__device__ __forceinline__ float across32(float x, OP op)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, x), __builtin_bit_cast(unsigned, x), false, false);
+    return op(__builtin_bit_cast(float, (unsigned)r[0]), __builtin_bit_cast(float, (unsigned)r[1]));
+}
+template <class OP>
+__device__ __forceinline__ float across16(float x, OP op)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, x), __builtin_bit_cast(unsigned, x), false, false);
+    return op(__builtin_bit_cast(float, (unsigned)r[0]), __builtin_bit_cast(float, (unsigned)r[1]));
+}
+struct Max {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct Add {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+
+// A 32-bit word that the whole wavefront reads from device memory that the
+// kernel does not write: one scalar load.
+__device__ __forceinline__ int uniform_word(const int32_t *p)
+{
+    typedef const int32_t __attribute__((address_space(4))) *cptr;
+    return *(cptr)(uintptr_t)p;
+}
+
 // Sizes in bytes of the three types.
 inline int type_size(int type) { return type == BQ_F32 ? 4 : 2; }
 
