@@ -31,29 +31,31 @@ __device__ __forceinline__ bool has_few(const AttnPlan &p, int rows)
     return p.many.tiles == 0 || (p.few.tiles && rows <= kFewRows);
 }
 
-// The keys and rows of one request, bounded by what the launch was given.
+// The keys and rows of one request (the same in all lanes), bounded by what the
+// launch was given.
 struct Request {
     int row0, n, keys;
 };
 __device__ __forceinline__ Request request_at(const bq_attn &a, int b)
 {
     Request r;
-    const int lo = a.cu[b], hi = a.cu[b + 1];
+    const int lo = uniform_word(a.cu + b), hi = uniform_word(a.cu + b + 1);
     r.row0 = lo < 0 ? 0 : lo;
     const int end = hi > a.tokens ? (int)a.tokens : hi;
     r.n = lo < 0 ? 0 : end - lo;  // a request that starts before the rows is none
     const int64_t most = (int64_t)a.table_cols * a.cache.page;
-    const int len = a.lens[b];
+    const int len = uniform_word(a.lens + b);
     r.keys = len < 0 ? 0 : len > most ? (int)most : len;
     return r;
 }
 
-// Page of key block `key` (a multiple of 8) of a request, -1 where there is none.
+// Page of the 16 keys from `key` (a multiple of 16, the same in all lanes) of a
+// request, -1 where there is none.
 __device__ __forceinline__ int page_at(const AttnArgs &g, const int32_t *table, int key, int end)
 {
     if (key >= end)
         return -1;
-    const int p = table[key >> g.page_log2];
+    const int p = uniform_word(table + (key >> g.page_log2));
     return (unsigned)p < (unsigned)g.a.cache.pages ? p : -1;
 }
 

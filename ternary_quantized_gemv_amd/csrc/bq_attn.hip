@@ -28,23 +28,26 @@
 namespace bq {
 
 constexpr int kAttnWaves = 4;
-constexpr int kAttnKeys = 32;  // keys of a wavefront at a time
-constexpr int kAttnStep = kAttnKeys * kAttnWaves;
+constexpr int kAttnKeys = 32;   // keys of a wavefront at a time
+constexpr int kAttnStep = 128;  // keys that a workgroup's wavefronts take at most at a time
 
-template <int CT, int D, int NT, bool F32>
-__global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
+// CW of the four wavefronts take 16 NT columns each, the others the same
+// columns over other keys.
+template <int CT, int D, int NT, int CW, bool F32>
+__global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(const AttnArgs g)
 {
     typedef typename Num<CT>::t T;
     typedef typename Num<CT>::v8 v8;
     constexpr int NP = F32 ? Parts<T>::n : 1;
     constexpr int DJ = D / 32, DT = D / 16;
-    constexpr int REGIONS = NT == 1 ? kAttnWaves : 1;  // few rows: a place per wavefront for its sums
-    __shared__ float sm[kAttnWaves][NT][16], sl[kAttnWaves][NT][16];
-    __shared__ float so[REGIONS][NT * 16][D + 4];
+    constexpr int KW = kAttnWaves / CW, COLS = 16 * NT * CW;  // wavefronts along the keys, rows of a tile
+    __shared__ float sm[KW][COLS], sl[KW][COLS];
+    __shared__ float so[KW][COLS][D + 4];
 
     const bq_attn &a = g.a;
     const AttnSplit &sp = g.p.few;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int cw = wave % CW, kw = wave / CW;
     const int c16 = lane & 15, q4 = lane >> 4;
     const int b = blockIdx.z, kh = blockIdx.x;
     const int tile = blockIdx.y / sp.chunks, chunk = blockIdx.y % sp.chunks;
@@ -55,20 +58,21 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
     const int rows = (int)rows64;
     const int64_t page_elems = ((int64_t)a.cache.heads << g.page_log2) * D;
     const int P = a.cache.page, pmask = P - 1;
-    const T *kbase = static_cast<const T *>(a.cache.k) + (int64_t)kh * P * D + 8 * q4;
-    const T *vbase = static_cast<const T *>(a.cache.v) + (int64_t)(kh * D + c16) * P;
-    const int32_t *table = a.table + (int64_t)b * a.ld_table;
     // K: this lane reads key 8 (c16 / 4) + c16 % 4 (+ 4); V: keys 8 q4 .. 8 q4 + 7
     const int kofs = 8 * (c16 >> 2), vofs = 8 * q4;
+    const T *kbase = static_cast<const T *>(a.cache.k) + (int64_t)kh * P * D + 8 * q4 + (c16 & 3) * D;
+    const T *vbase = static_cast<const T *>(a.cache.v) + (int64_t)(kh * D + c16) * P;
+    const int32_t *table = a.table + (int64_t)b * a.ld_table;
 
-    for (int r0 = tile * 16 * NT; r0 < rows; r0 += sp.tiles * 16 * NT) {
-        // ---- the rows: this lane's columns are rows r0 + 16 t + c16
+    for (int r0 = tile * COLS; r0 < rows; r0 += sp.tiles * COLS) {
+        // ---- the rows: this lane's columns are rows c0 + 16 t + c16
+        const int c0 = r0 + 16 * NT * cw;
         v8 qf[NT][NP][DJ];
         float qs[NT], m[NT], l[NT];
         int last[NT];  // the last key the column sees
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int r = r0 + 16 * t + c16;
+            const int r = c0 + 16 * t + c16;
             const bool live = r < rows;
             const int i = live ? r / g.group : 0, hq = kh * g.group + (live ? r % g.group : 0);
             last[t] = live ? rq.keys - rq.n + i : -1;
@@ -85,38 +89,42 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
                 o[t][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
         // ---- the keys: those that the tile's last row sees, this workgroup's chunk of them
-        const int last_row = min(r0 + 16 * NT, rows) - 1;
+        const int last_row = min(r0 + COLS, rows) - 1;
         const int seen = min(rq.keys, rq.keys - rq.n + last_row / g.group + 1);
         const int begin = chunk * sp.chunk;
         const int end = chunk == sp.chunks - 1 ? seen : min(seen, begin + sp.chunk);
         const int first_last = rq.keys - rq.n + r0 / g.group;  // the last key that the tile's first row sees
 
         // pages one step ahead of the keys, keys and values one product ahead of their use
-        int k0 = begin + kAttnKeys * wave;
-        int kp = page_at(g, table, k0 + kofs, end), vp = page_at(g, table, k0 + vofs, end);
         v8 kf[2][DJ], vf[DT];
-        auto load_k = [&](int at, int page) {
-            const T *p = kbase + (int64_t)max(page, 0) * page_elems + (((at + kofs) & pmask) + (c16 & 3)) * D;
+        auto load_k = [&](int at, int page0, int page1) {
+            const int page = max(c16 < 8 ? page0 : page1, 0);
+            const T *p = kbase + (int64_t)page * page_elems + ((at + kofs) & pmask) * D;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int j = 0; j < DJ; ++j)
                     kf[t][j] = *reinterpret_cast<const v8 *>(p + 4 * t * D + 32 * j);
         };
-        auto load_v = [&](int at, int page) {
-            const T *p = vbase + (int64_t)max(page, 0) * page_elems + ((at + vofs) & pmask);
+        auto load_v = [&](int at, int page0, int page1) {
+            const int page = max(q4 < 2 ? page0 : page1, 0);
+            const T *p = vbase + (int64_t)page * page_elems + ((at + vofs) & pmask);
 #pragma unroll
             for (int d = 0; d < DT; ++d)
                 vf[d] = *reinterpret_cast<const v8 *>(p + 16 * d * P);
         };
+        int k0 = begin + kAttnKeys * kw;
+        int p0 = page_at(g, table, k0, end), p1 = page_at(g, table, k0 + 16, end);
+        constexpr int STEP = kAttnKeys * KW;
+        int n0 = page_at(g, table, k0 + STEP, end), n1 = page_at(g, table, k0 + STEP + 16, end);
         if (k0 < end) {
-            load_k(k0, kp);
-            load_v(k0, vp);
+            load_k(k0, p0, p1);
+            load_v(k0, p0, p1);
         }
         while (k0 < end) {
-            const int next = k0 + kAttnStep;
-            const int nkp = page_at(g, table, next + kofs, end), nvp = page_at(g, table, next + vofs, end);
-            const bool whole = k0 + kAttnKeys - 1 <= first_last && k0 + kAttnKeys <= end && !__any(kp < 0);
+            const int next = k0 + STEP;
+            const bool whole = k0 + kAttnKeys - 1 <= first_last && k0 + kAttnKeys <= end && p0 >= 0 && p1 >= 0;
+            const bool here = (q4 < 2 ? p0 : p1) >= 0;  // this lane's keys have a page
             f32x4 s[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -130,14 +138,14 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
                             s[t][h] = Num<CT>::mfma16(kf[h][j], qf[t][p][j], s[t][h]);
                 }
             if (next < end)
-                load_k(next, nkp);
+                load_k(next, n0, n1);
             if (!whole) {
                 // places that no row sees may hold anything: their values must not meet a weight of 0
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        vf[d][e] = k0 + vofs + e < end && vp >= 0 ? vf[d][e] : (T)0.0f;
+                        vf[d][e] = k0 + vofs + e < end && here ? vf[d][e] : (T)0.0f;
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -149,7 +157,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int key = k0 + vofs + e;
-                        w[e] = key <= last[t] && key < end && vp >= 0 ? w[e] * factor : kNone;
+                        w[e] = key <= last[t] && key < end && here ? w[e] * factor : kNone;
                     }
                     factor = 1.0f;
                 }
@@ -186,71 +194,48 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
                         o[t][d] = Num<CT>::mfma16(vf[d], pf[p], o[t][d]);
             }
             if (next < end)
-                load_v(next, nvp);
+                load_v(next, n0, n1);
+            p0 = n0;
+            p1 = n1;
+            n0 = page_at(g, table, next + STEP, end);
+            n1 = page_at(g, table, next + STEP + 16, end);
             k0 = next;
-            kp = nkp;
-            vp = nvp;
         }
-        // ---- the four wavefronts' sums become one; l over the lane's key groups first
+        // ---- the sums of the wavefronts along the keys become one; l over the lane's key groups first
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             l[t] = across32(across16(l[t], Add()), Add());
+            const int col = 16 * (NT * cw + t) + c16;
             if (q4 == 0) {
-                sm[wave][t][c16] = m[t];
-                sl[wave][t][c16] = l[t];
+                sm[kw][col] = m[t];
+                sl[kw][col] = l[t];
             }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float mt = kNone;
-#pragma unroll
-            for (int w = 0; w < kAttnWaves; ++w)
-                mt = fmaxf(mt, sm[w][t][c16]);
-            const float f = __builtin_amdgcn_exp2f(m[t] - (mt == kNone ? 0.0f : mt));
 #pragma unroll
             for (int d = 0; d < DT; ++d)
-                o[t][d] *= f;
+                *reinterpret_cast<f32x4 *>(&so[kw][col][16 * d + 4 * q4]) = o[t][d];
         }
-        for (int w = 0; w < kAttnWaves; ++w) {
-            if (wave == w) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) {
-                        f32x4 *p = reinterpret_cast<f32x4 *>(&so[REGIONS > 1 ? w : 0][16 * t + c16][16 * d + 4 * q4]);
-                        *p = w && REGIONS == 1 ? *p + o[t][d] : o[t][d];
-                    }
-            }
-            if (REGIONS == 1)
-                __syncthreads();
-        }
-        if (REGIONS > 1)
-            __syncthreads();
+        __syncthreads();
         // ---- out, or this chunk's part of it
-        for (int u = threadIdx.x; u < 16 * NT * (D / 8); u += 64 * kAttnWaves) {
+        for (int u = threadIdx.x; u < COLS * (D / 8); u += 64 * kAttnWaves) {
             const int cr = u / (D / 8), d8 = u % (D / 8) * 8, r = r0 + cr;
             if (r >= rows)
                 continue;
             const int64_t tok = rq.row0 + r / g.group;
             const int hq = kh * g.group + r % g.group;
-            float v[8], mt = kNone, lt = 0.0f;
-            load8(&so[0][cr][d8], v);
+            float v[8] = {}, mt = kNone, lt = 0.0f;
 #pragma unroll
-            for (int w = 1; w < REGIONS; ++w) {
+            for (int w = 0; w < KW; ++w)
+                mt = fmaxf(mt, sm[w][cr]);
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {
+                const float f = __builtin_amdgcn_exp2f(sm[w][cr] - (mt == kNone ? 0.0f : mt));
                 float x[8];
                 load8(&so[w][cr][d8], x);
+                lt = __builtin_fmaf(sl[w][cr], f, lt);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[e] += x[e];
+                    v[e] = __builtin_fmaf(x[e], f, v[e]);
             }
-#pragma unroll
-            for (int w = 0; w < kAttnWaves; ++w)
-                mt = fmaxf(mt, sm[w][cr >> 4][cr & 15]);
-            const float mz = mt == kNone ? 0.0f : mt;
-#pragma unroll
-            for (int w = 0; w < kAttnWaves; ++w)
-                lt += sl[w][cr >> 4][cr & 15] * __builtin_amdgcn_exp2f(sm[w][cr >> 4][cr & 15] - mz);
             if (sp.chunks == 1) {
                 const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
 #pragma unroll
@@ -271,72 +256,115 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_kernel(const AttnArgs g)
     }
 }
 
-// The pieces of a row added up, one workgroup a row: the lanes of a wavefront
+// The pieces of a request of few rows added up, a workgroup a row: the lanes of a wavefront
 // hold the pieces' statistics (at most 128), then D / 8 threads take every
 // 256 / (D / 8)-th piece's sums and add up through LDS, always in that order.
 constexpr int kMaxChunks = 128;
 
 template <class OT, int D>
-__global__ __launch_bounds__(256) void attn_join(const AttnArgs g)
+__global__ __launch_bounds__(256) void attn_join_few(const AttnArgs g)
 {
     const bq_attn &a = g.a;
     constexpr int L = D / 8, GROUPS = 256 / L;
     __shared__ float weight[kMaxChunks];
     __shared__ float so[GROUPS][D + 4];
-    const int64_t row = blockIdx.x, tok = row / a.q_heads;
-    const int hq = (int)(row % a.q_heads);
+    const Request rq = request_at(a, blockIdx.y);
+    const int chunks = g.p.few.chunks;
+    const int64_t rows64 = (int64_t)rq.n * g.group;
+    if (rq.n <= 0 || !has_few(g.p, (int)rows64))
+        return;
+    const int lane = threadIdx.x & 63;
+    for (int64_t u = blockIdx.x; u < (int64_t)rq.n * a.q_heads; u += gridDim.x) {
+        const int64_t row = (int64_t)rq.row0 * a.q_heads + u;
+        const float2 none = make_float2(kNone, 0.0f);
+        const float2 s0 = lane < chunks ? *part_stats(g, row, lane, D) : none;
+        const float2 s1 = lane + 64 < chunks ? *part_stats(g, row, lane + 64, D) : none;
+        float m = fmaxf(s0.x, s1.x);
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1)
+            m = fmaxf(m, __shfl_xor(m, off, 64));
+        m = m == kNone ? 0.0f : m;
+        const float f0 = __builtin_amdgcn_exp2f(s0.x - m), f1 = __builtin_amdgcn_exp2f(s1.x - m);
+        float l = s0.y * f0 + s1.y * f1;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1)
+            l += __shfl_xor(l, off, 64);
+        if (threadIdx.x < 64) {
+            weight[lane] = f0;
+            weight[lane + 64] = f1;
+        }
+        __syncthreads();
+        const int grp = threadIdx.x / L, d8 = threadIdx.x % L * 8;
+        float o[8] = {};
+        for (int c = grp; c < chunks; c += GROUPS) {
+            float v[8];
+            load8(part_sums(g, row, c, D) + d8, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o[e] = __builtin_fmaf(v[e], weight[c], o[e]);
+        }
+        store8(&so[grp][d8], o);
+        __syncthreads();
+        if (grp == 0) {
+            const int groups = min(GROUPS, chunks);
+            for (int k = 1; k < groups; ++k) {
+                float v[8];
+                load8(&so[k][d8], v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    o[e] += v[e];
+            }
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o[e] *= inv;
+            store8(static_cast<OT *>(a.out) + row / a.q_heads * a.ld_out + row % a.q_heads * D + d8, o);
+        }
+        __syncthreads();
+    }
+}
+
+// The pieces of requests of many rows added up: D / 8 lanes a row.
+template <class OT, int D>
+__global__ __launch_bounds__(256) void attn_join_many(const AttnArgs g)
+{
+    const bq_attn &a = g.a;
+    constexpr int L = D / 8;
+    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
+    const int d8 = threadIdx.x % L * 8, chunks = g.p.many.chunks;
+    if (row >= a.tokens * a.q_heads)
+        return;
+    const int64_t tok = row / a.q_heads;
     const int b = request_of(a.cu, a.requests, (int)tok);
     if (b < 0)
         return;
-    const int64_t rows = (int64_t)request_at(a, b).n * g.group;
-    const int chunks = has_few(g.p, (int)rows) ? g.p.few.chunks : g.p.many.chunks;
-    if (chunks == 1)
+    // as request_at counts them
+    const int lo = a.cu[b], hi = a.cu[b + 1];
+    const int64_t n = lo < 0 ? 0 : (hi > a.tokens ? a.tokens : hi) - lo;
+    if (n <= 0 || has_few(g.p, (int)(n * g.group)))
         return;
-    const int lane = threadIdx.x & 63;
-    const float2 none = make_float2(kNone, 0.0f);
-    const float2 s0 = lane < chunks ? *part_stats(g, row, lane, D) : none;
-    const float2 s1 = lane + 64 < chunks ? *part_stats(g, row, lane + 64, D) : none;
-    float m = fmaxf(s0.x, s1.x);
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1)
-        m = fmaxf(m, __shfl_xor(m, off, 64));
+    const float *sums = part_sums(g, row, 0, D) + d8;
+    const float2 *stats = part_stats(g, row, 0, D);
+    float m = kNone;
+    for (int c = 0; c < chunks; ++c)
+        m = fmaxf(m, stats[c].x);
     m = m == kNone ? 0.0f : m;
-    const float f0 = __builtin_amdgcn_exp2f(s0.x - m), f1 = __builtin_amdgcn_exp2f(s1.x - m);
-    float l = s0.y * f0 + s1.y * f1;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1)
-        l += __shfl_xor(l, off, 64);
-    if (threadIdx.x < 64) {
-        weight[lane] = f0;
-        weight[lane + 64] = f1;
-    }
-    __syncthreads();
-    const int grp = threadIdx.x / L, d8 = threadIdx.x % L * 8;
-    float o[8] = {};
-    for (int c = grp; c < chunks; c += GROUPS) {
+    float l = 0.0f, o[8] = {};
+#pragma unroll 4
+    for (int c = 0; c < chunks; ++c) {
+        const float f = __builtin_amdgcn_exp2f(stats[c].x - m);
         float v[8];
-        load8(part_sums(g, row, c, D) + d8, v);
+        load8(sums + (int64_t)c * D, v);
+        l = __builtin_fmaf(stats[c].y, f, l);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            o[e] = __builtin_fmaf(v[e], weight[c], o[e]);
-    }
-    store8(&so[grp][d8], o);
-    __syncthreads();
-    if (grp)
-        return;
-    const int groups = min(GROUPS, chunks);
-    for (int k = 1; k < groups; ++k) {
-        float v[8];
-        load8(&so[k][d8], v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            o[e] += v[e];
+            o[e] = __builtin_fmaf(v[e], f, o[e]);
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         o[e] *= inv;
-    store8(static_cast<OT *>(a.out) + tok * a.ld_out + (int64_t)hq * D + d8, o);
+    store8(static_cast<OT *>(a.out) + tok * a.ld_out + (row - tok * a.q_heads) * D + d8, o);
 }
 
 // Pieces of the keys so that about `want` workgroups run, none of fewer than
@@ -388,9 +416,9 @@ template <int CT, int D, bool F32>
 static void attn_nt(const AttnArgs &g, dim3 grid, hipStream_t st)
 {
     switch (g.p.few.cols) {
-    case 16: hipLaunchKernelGGL((attn_kernel<CT, D, 1, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
-    case 32: hipLaunchKernelGGL((attn_kernel<CT, D, 2, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
-    default: hipLaunchKernelGGL((attn_kernel<CT, D, 4, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
+    case 16: hipLaunchKernelGGL((attn_kernel<CT, D, 1, 1, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
+    case 32: hipLaunchKernelGGL((attn_kernel<CT, D, 1, 2, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
+    default: hipLaunchKernelGGL((attn_kernel<CT, D, 2, 2, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
     }
 }
 
@@ -401,14 +429,24 @@ static void attn_dim(const AttnArgs &g, dim3 grid, hipStream_t st)
     f32 ? attn_nt<CT, D, true>(g, grid, st) : attn_nt<CT, D, false>(g, grid, st);
 }
 
+template <class OT, int D>
+static void join_type(const AttnArgs &g, hipStream_t st)
+{
+    const bq_attn &a = g.a;
+    if (g.p.few.chunks > 1) {
+        const int64_t most = (int64_t)g.p.few.tiles * g.p.few.cols * a.cache.heads;
+        hipLaunchKernelGGL((attn_join_few<OT, D>), dim3((unsigned)most, (unsigned)a.requests), dim3(256), 0, st, g);
+    }
+    if (g.p.many.chunks > 1) {
+        const int64_t blocks = (a.tokens * a.q_heads * (D / 8) + 255) / 256;
+        hipLaunchKernelGGL((attn_join_many<OT, D>), dim3((unsigned)blocks), dim3(256), 0, st, g);
+    }
+}
+
 template <int CT, int D>
 static void join_dim(const AttnArgs &g, hipStream_t st)
 {
-    const dim3 grid((unsigned)(g.a.tokens * g.a.q_heads));
-    if (g.a.type == BQ_F32)
-        hipLaunchKernelGGL((attn_join<float, D>), grid, dim3(256), 0, st, g);
-    else
-        hipLaunchKernelGGL((attn_join<typename Num<CT>::t, D>), grid, dim3(256), 0, st, g);
+    g.a.type == BQ_F32 ? join_type<float, D>(g, st) : join_type<typename Num<CT>::t, D>(g, st);
 }
 
 hipError_t launch_attn(const bq_attn &a, const AttnPlan &p, hipStream_t st)

@@ -94,19 +94,16 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
         int page[BLOCKS];
         auto look_up = [&](int k0) {
 #pragma unroll
-            for (int i = 0; i < BLOCKS; ++i) {
-                const int key = k0 + 16 * i;
-                const int p = key < end ? uniform_word(table + (key >> g.page_log2)) : -1;
-                page[i] = (unsigned)p < (unsigned)a.cache.pages ? p : -1;
-            }
+            for (int i = 0; i < BLOCKS; ++i)
+                page[i] = page_at(g, table, k0 + 16 * i, end);
         };
-        bool holes = false, bad = false;  // a page of this (the next) tile is outside the cache, or it ends early
+        int holes = 0, bad = 0;  // 16-key blocks of this (the next) tile without a page of the cache
         int vpage = -1;
         auto fetch = [&](int k0) {
-            bad = false;
+            bad = 0;
 #pragma unroll
             for (int i = 0; i < BLOCKS; ++i)
-                bad |= page[i] < 0;
+                bad |= (page[i] < 0) << i;
 #pragma unroll
             for (int i = 0; i < KL; ++i) {
                 const int row = kr + KROWS * i, ri = row & 31;
@@ -184,7 +181,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int key = k0 + 32 * h + 16 * (e >> 3) + 8 * half + (e & 7);
-                        const bool sees = key <= last && key < end && (!holes || page_at(g, table, key, end) >= 0);
+                        const bool sees = key <= last && key < end && !(holes >> (2 * h + (e >> 3)) & 1);
                         s[e] = sees ? s[e] * factor : kNone;
                     }
                     factor = 1.0f;
