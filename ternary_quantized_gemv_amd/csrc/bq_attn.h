@@ -28,7 +28,7 @@ struct AttnArgs {
 constexpr int kFewRows = 64;
 __device__ __forceinline__ bool has_few(const AttnPlan &p, int rows)
 {
-    return p.many.tiles == 0 || (p.few.tiles && rows <= kFewRows);
+    return p.many.tiles == 0 || (p.few.cols && rows <= kFewRows);
 }
 
 // The keys and rows of one request (the same in all lanes), bounded by what the

@@ -30,11 +30,123 @@ namespace bq {
 constexpr int kAttnWaves = 4;
 constexpr int kAttnKeys = 32;   // keys of a wavefront at a time
 constexpr int kAttnStep = 128;  // keys that a workgroup's wavefronts take at most at a time
+constexpr int kMaxChunks = 128; // pieces of a row's keys that the joins take
+
+// ---- the split of the keys, from the lengths of all requests
+//
+// Requests of very different lengths would leave some compute units with long
+// ones and others with none (pieces of a fixed number of keys, empty ones
+// among them: 75 us against 61 for 32 requests of 3 to 8192 keys), so every
+// workgroup derives the same equal cut from the lengths: units of 128 keys,
+// `chunk` of them a piece, so that the pieces are about few.items per key head
+// and at most g.p.stride per row.
+
+// Lane i: tiles of rows and units of keys of request `i` (0 if it is not this kernel's).
+__device__ __forceinline__ void few_request(const AttnArgs &g, int i, int &tiles, int &units)
+{
+    tiles = units = 0;
+    if (i >= g.a.requests)
+        return;
+    const int lo = g.a.cu[i], hi = g.a.cu[i + 1], len = g.a.lens[i];
+    const int n = lo < 0 ? 0 : (hi > g.a.tokens ? (int)g.a.tokens : hi) - lo;
+    const int64_t most = (int64_t)g.a.table_cols * g.a.cache.page, rows = (int64_t)n * g.group;
+    if (n <= 0 || !has_few(g.p, (int)rows))
+        return;
+    tiles = ((int)rows + g.p.few.cols - 1) / g.p.few.cols;
+    units = ((len > most ? (int)most : len) + kAttnStep - 1) / kAttnStep;
+    units = units < 1 ? 1 : units;  // no keys: one piece, of zeros
+}
+
+__device__ __forceinline__ float wave_sum(float x)
+{
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+        x += __shfl_xor(x, off, 64);
+    return x;
+}
+
+// Units of a piece: those of all requests over the pieces wanted, and, as every
+// request rounds its pieces up, more where that made too many (twice: pieces
+// that fill the GPU once and a third take as long as two fillings).  Sums in
+// f32: the same in every workgroup, and exact enough.
+__device__ __forceinline__ int few_chunk(const AttnArgs &g, int tiles0, int units0)
+{
+    const int lane = threadIdx.x & 63;
+    const float want = (float)g.p.few.items;
+    float total = (float)tiles0 * (float)units0;
+    int most = units0;
+    for (int base = 64; base < g.a.requests; base += 64) {
+        int t, u;
+        few_request(g, base + lane, t, u);
+        total += (float)t * (float)u;
+        most = max(most, u);
+    }
+    if (g.a.requests > 1) {
+        total = wave_sum(total);
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1)
+            most = max(most, __shfl_xor(most, off, 64));
+    }
+    const int least = max((most + g.p.stride - 1) / g.p.stride, 1);
+    int chunk = max((int)fminf(__builtin_ceilf(total / want), 16777216.0f), least);
+    if (g.a.requests > 1) {
+        for (int again = 0; again < 2; ++again) {
+            float count = (float)(tiles0 * ((units0 + chunk - 1) / chunk));
+            for (int base = 64; base < g.a.requests; base += 64) {
+                int t, u;
+                few_request(g, base + lane, t, u);
+                count += (float)(t * ((u + chunk - 1) / chunk));
+            }
+            count = wave_sum(count);
+            if (count > want)
+                chunk = min(max((int)fminf(__builtin_ceilf((float)chunk * (count / want)), 16777216.0f), chunk + 1), max(most, least));
+        }
+    }
+    return __builtin_amdgcn_readfirstlane(chunk);
+}
+
+// Item `item` of the pieces of all requests: request b, its tile and chunk, how
+// many chunks it has and the keys of each (a request's pieces are as even as
+// its units allow).  False where there are fewer items.
+__device__ __forceinline__ bool few_item(const AttnArgs &g, int item, int chunk_units, int tiles0, int units0, int &b,
+                                         int &tile, int &chunk, int &chunks, int &keys)
+{
+    const int lane = threadIdx.x & 63;
+    int before = 0;  // items of the requests in front
+    for (int base = 0; base < g.a.requests; base += 64) {
+        int t = tiles0, u = units0;
+        if (base)
+            few_request(g, base + lane, t, u);
+        const int c = (u + chunk_units - 1) / chunk_units, mine = t * c;
+        int upto = mine;
+        if (g.a.requests > 1) {
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const int x = __shfl_up(upto, off, 64);
+                upto += lane >= off ? x : 0;
+            }
+        }
+        const unsigned long long has = __ballot(item - before < upto);
+        if (has) {
+            const int at = __builtin_ctzll(has);
+            b = base + at;
+            const int within = item - before - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at));
+            const int ts = __builtin_amdgcn_readlane(t, at);
+            chunks = __builtin_amdgcn_readlane(c, at);
+            keys = (__builtin_amdgcn_readlane(u, at) + chunks - 1) / chunks * kAttnStep;
+            tile = within % ts;
+            chunk = within / ts;
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return false;
+}
 
 // CW of the four wavefronts take 16 NT columns each, the others the same
 // columns over other keys.
 template <int CT, int D, int NT, int CW, bool F32>
-__global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(const AttnArgs g)
+__global__ __launch_bounds__(64 * kAttnWaves, NT == 1 && !F32 ? 3 : 2) void attn_kernel(const AttnArgs g)
 {
     typedef typename Num<CT>::t T;
     typedef typename Num<CT>::v8 v8;
@@ -45,27 +157,59 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(const AttnArgs
     __shared__ float so[KW][COLS][D + 4];
 
     const bq_attn &a = g.a;
-    const AttnSplit &sp = g.p.few;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cw = wave % CW, kw = wave / CW;
     const int c16 = lane & 15, q4 = lane >> 4;
-    const int b = blockIdx.z, kh = blockIdx.x;
-    const int tile = blockIdx.y / sp.chunks, chunk = blockIdx.y % sp.chunks;
-    const Request rq = request_at(a, b);
-    const int64_t rows64 = (int64_t)rq.n * g.group;
-    if (rq.n <= 0 || !has_few(g.p, (int)rows64))
-        return;
-    const int rows = (int)rows64;
+    const int kh = blockIdx.x;
     const int64_t page_elems = ((int64_t)a.cache.heads << g.page_log2) * D;
     const int P = a.cache.page, pmask = P - 1;
     // K: this lane reads key 8 (c16 / 4) + c16 % 4 (+ 4); V: keys 8 q4 .. 8 q4 + 7
     const int kofs = 8 * (c16 >> 2), vofs = 8 * q4;
     const T *kbase = static_cast<const T *>(a.cache.k) + (int64_t)kh * P * D + 8 * q4 + (c16 & 3) * D;
     const T *vbase = static_cast<const T *>(a.cache.v) + (int64_t)(kh * D + c16) * P;
-    const int32_t *table = a.table + (int64_t)b * a.ld_table;
+    int tiles0, units0;
+    few_request(g, lane, tiles0, units0);
+    const int chunk_units = few_chunk(g, tiles0, units0);
 
-    for (int r0 = tile * COLS; r0 < rows; r0 += sp.tiles * COLS) {
-        // ---- the rows: this lane's columns are rows c0 + 16 t + c16
+    int b, tile, chunk, chunks, keys;
+    for (int item = blockIdx.y; few_item(g, item, chunk_units, tiles0, units0, b, tile, chunk, chunks, keys); item += gridDim.y) {
+        const Request rq = request_at(a, b);
+        const int rows = rq.n * g.group, r0 = tile * COLS;
+        const int32_t *table = a.table + (int64_t)b * a.ld_table;
+        // ---- the keys: those that the tile's last row sees, this workgroup's chunk of them
+        const int last_row = min(r0 + COLS, rows) - 1;
+        const int seen = min(rq.keys, rq.keys - rq.n + last_row / g.group + 1);
+        const int begin = chunk * keys;
+        const int end = min(seen, begin + keys);
+        const int first_last = rq.keys - rq.n + r0 / g.group;  // the last key that the tile's first row sees
+
+        // pages one step ahead of the keys, keys and values one product ahead of their use
+        v8 kf[2][DJ], vf[DT];
+        auto load_k = [&](int at, int page0, int page1) {
+            const int page = max(c16 < 8 ? page0 : page1, 0);
+            const T *p = kbase + (int64_t)page * page_elems + ((at + kofs) & pmask) * D;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int j = 0; j < DJ; ++j)
+                    kf[t][j] = stream8<v8, CW == 1>(p + 4 * t * D + 32 * j);
+        };
+        auto load_v = [&](int at, int page0, int page1) {
+            const int page = max(q4 < 2 ? page0 : page1, 0);
+            const T *p = vbase + (int64_t)page * page_elems + ((at + vofs) & pmask);
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                vf[d] = stream8<v8, CW == 1>(p + 16 * d * P);
+        };
+        int k0 = begin + kAttnKeys * kw;
+        int p0 = page_at(g, table, k0, end), p1 = page_at(g, table, k0 + 16, end);
+        constexpr int STEP = kAttnKeys * KW;
+        int n0 = page_at(g, table, k0 + STEP, end), n1 = page_at(g, table, k0 + STEP + 16, end);
+        if (k0 < end) {
+            load_k(k0, p0, p1);
+            load_v(k0, p0, p1);
+        }
+        // ---- the rows, behind the first keys in the queue of loads: this lane's columns are rows c0 + 16 t + c16
         const int c0 = r0 + 16 * NT * cw;
         v8 qf[NT][NP][DJ];
         float qs[NT], m[NT], l[NT];
@@ -88,39 +232,6 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(const AttnArgs
             for (int d = 0; d < DT; ++d)
                 o[t][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-        // ---- the keys: those that the tile's last row sees, this workgroup's chunk of them
-        const int last_row = min(r0 + COLS, rows) - 1;
-        const int seen = min(rq.keys, rq.keys - rq.n + last_row / g.group + 1);
-        const int begin = chunk * sp.chunk;
-        const int end = chunk == sp.chunks - 1 ? seen : min(seen, begin + sp.chunk);
-        const int first_last = rq.keys - rq.n + r0 / g.group;  // the last key that the tile's first row sees
-
-        // pages one step ahead of the keys, keys and values one product ahead of their use
-        v8 kf[2][DJ], vf[DT];
-        auto load_k = [&](int at, int page0, int page1) {
-            const int page = max(c16 < 8 ? page0 : page1, 0);
-            const T *p = kbase + (int64_t)page * page_elems + ((at + kofs) & pmask) * D;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int j = 0; j < DJ; ++j)
-                    kf[t][j] = *reinterpret_cast<const v8 *>(p + 4 * t * D + 32 * j);
-        };
-        auto load_v = [&](int at, int page0, int page1) {
-            const int page = max(q4 < 2 ? page0 : page1, 0);
-            const T *p = vbase + (int64_t)page * page_elems + ((at + vofs) & pmask);
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-                vf[d] = *reinterpret_cast<const v8 *>(p + 16 * d * P);
-        };
-        int k0 = begin + kAttnKeys * kw;
-        int p0 = page_at(g, table, k0, end), p1 = page_at(g, table, k0 + 16, end);
-        constexpr int STEP = kAttnKeys * KW;
-        int n0 = page_at(g, table, k0 + STEP, end), n1 = page_at(g, table, k0 + STEP + 16, end);
-        if (k0 < end) {
-            load_k(k0, p0, p1);
-            load_v(k0, p0, p1);
-        }
         while (k0 < end) {
             const int next = k0 + STEP;
             const bool whole = k0 + kAttnKeys - 1 <= first_last && k0 + kAttnKeys <= end && p0 >= 0 && p1 >= 0;
@@ -236,7 +347,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(const AttnArgs
                 for (int e = 0; e < 8; ++e)
                     v[e] = __builtin_fmaf(x[e], f, v[e]);
             }
-            if (sp.chunks == 1) {
+            if (chunks == 1) {
                 const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -257,26 +368,40 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void attn_kernel(const AttnArgs
 }
 
 // The pieces of a request of few rows added up, a workgroup a row: the lanes of a wavefront
-// hold the pieces' statistics (at most 128), then D / 8 threads take every
+// hold the pieces' statistics, then D / 8 threads take every
 // 256 / (D / 8)-th piece's sums and add up through LDS, always in that order.
-constexpr int kMaxChunks = 128;
-
 template <class OT, int D>
 __global__ __launch_bounds__(256) void attn_join_few(const AttnArgs g)
 {
     const bq_attn &a = g.a;
-    constexpr int L = D / 8, GROUPS = 256 / L;
+    constexpr int L = D / 8, GROUPS = 256 / L, MOST = kMaxChunks / GROUPS;
     __shared__ float weight[kMaxChunks];
     __shared__ float so[GROUPS][D + 4];
-    const Request rq = request_at(a, blockIdx.y);
-    const int chunks = g.p.few.chunks;
-    const int64_t rows64 = (int64_t)rq.n * g.group;
-    if (rq.n <= 0 || !has_few(g.p, (int)rows64))
-        return;
     const int lane = threadIdx.x & 63;
+    const Request rq = request_at(a, blockIdx.y);
+    const int64_t rows64 = (int64_t)rq.n * g.group;
+    if (rq.n <= 0 || !has_few(g.p, (int)rows64) || (int64_t)blockIdx.x >= (int64_t)rq.n * a.q_heads)
+        return;
+    int tiles0, units0;
+    few_request(g, lane, tiles0, units0);
+    const int chunk_units = few_chunk(g, tiles0, units0);
+    const int chunks = ((rq.keys + kAttnStep - 1) / kAttnStep + chunk_units - 1) / chunk_units;
+    if (chunks <= 1)
+        return;
+    const int grp = threadIdx.x / L, d8 = threadIdx.x % L * 8;
     for (int64_t u = blockIdx.x; u < (int64_t)rq.n * a.q_heads; u += gridDim.x) {
         const int64_t row = (int64_t)rq.row0 * a.q_heads + u;
         const float2 none = make_float2(kNone, 0.0f);
+        // all loads first: a single token waits for little else
+        float v[MOST][8];
+#pragma unroll
+        for (int i = 0; i < MOST; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[i][e] = 0.0f;
+            if (grp + GROUPS * i < chunks)
+                load8(part_sums(g, row, grp + GROUPS * i, D) + d8, v[i]);
+        }
         const float2 s0 = lane < chunks ? *part_stats(g, row, lane, D) : none;
         const float2 s1 = lane + 64 < chunks ? *part_stats(g, row, lane + 64, D) : none;
         float m = fmaxf(s0.x, s1.x);
@@ -294,25 +419,24 @@ __global__ __launch_bounds__(256) void attn_join_few(const AttnArgs g)
             weight[lane + 64] = f1;
         }
         __syncthreads();
-        const int grp = threadIdx.x / L, d8 = threadIdx.x % L * 8;
         float o[8] = {};
-        for (int c = grp; c < chunks; c += GROUPS) {
-            float v[8];
-            load8(part_sums(g, row, c, D) + d8, v);
+#pragma unroll
+        for (int i = 0; i < MOST; ++i) {
+            const float f = weight[grp + GROUPS * i];  // 0 where there is no piece
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                o[e] = __builtin_fmaf(v[e], weight[c], o[e]);
+                o[e] = __builtin_fmaf(v[i][e], f, o[e]);
         }
         store8(&so[grp][d8], o);
         __syncthreads();
         if (grp == 0) {
             const int groups = min(GROUPS, chunks);
             for (int k = 1; k < groups; ++k) {
-                float v[8];
-                load8(&so[k][d8], v);
+                float x[8];
+                load8(&so[k][d8], x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    o[e] += v[e];
+                    o[e] += x[e];
             }
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
@@ -367,47 +491,49 @@ __global__ __launch_bounds__(256) void attn_join_many(const AttnArgs g)
     store8(static_cast<OT *>(a.out) + tok * a.ld_out + (row - tok * a.q_heads) * D + d8, o);
 }
 
-// Pieces of the keys so that about `want` workgroups run, none of fewer than
-// `least` keys.
-static void split_keys(AttnSplit &s, const bq_attn &a, int64_t want, int64_t least)
-{
-    const int64_t group = a.q_heads / a.cache.heads;
-    // tiles that can have rows: no request has more than s.tiles, all together no more than the rows allow
-    const int64_t all = a.tokens * group / s.cols + a.requests, each = (int64_t)s.tiles * a.requests;
-    const int64_t busy = (each < all ? each : all) * a.cache.heads;
-    int64_t chunks = want / (busy < 1 ? 1 : busy);
-    const int64_t steps = (a.max_keys + least - 1) / least;
-    chunks = chunks > steps ? steps : chunks;
-    chunks = chunks > kMaxChunks ? kMaxChunks : chunks;
-    if (chunks < 1)
-        chunks = 1;
-    const int64_t per = steps < 1 ? 1 : (steps + chunks - 1) / chunks;
-    s.chunk = (int)(per * least);
-    s.chunks = (int)(steps < 1 ? 1 : (steps + per - 1) / per);
-}
-
 AttnPlan attn_plan(const bq_attn &a)
 {
     AttnPlan p;
-    const int group = a.q_heads / a.cache.heads;
+    const int64_t group = a.q_heads / a.cache.heads, heads = a.cache.heads;
     const int64_t most = a.max_new < a.tokens ? a.max_new : a.tokens;
     const int64_t rows = most * group;
+    p.few.cols = p.few.grid = p.few.items = 0;
     p.many.cols = p.many.tiles = p.many.chunk = 0;
     p.many.chunks = 1;
-    p.few.cols = rows <= 16 || rows > kFewRows ? 16 : rows <= 32 ? 32 : 64;
-    p.few.tiles = (int)(((rows > kFewRows ? kFewRows : rows) + p.few.cols - 1) / p.few.cols);
-    split_keys(p.few, a, 2048, kAttnStep);
-    if (rows > kFewRows && a.requests == 1) {  // one request: one kernel
-        p.few.tiles = 0;
-        p.few.chunks = 1;
+    int64_t stride = 1;
+    if (rows <= kFewRows || a.requests > 1) {  // one request of many rows: one kernel
+        p.few.cols = rows <= 16 || rows > kFewRows ? 16 : rows <= 32 ? 32 : 64;
+        const int64_t tiles = ((rows > kFewRows ? kFewRows : rows) + p.few.cols - 1) / p.few.cols;
+        const int64_t units = (a.max_keys + kAttnStep - 1) / kAttnStep;
+        // as many pieces as workgroups fit the 256 compute units at once: three where 170 registers allow it
+        const int64_t want = p.few.cols == 16 && a.type != BQ_F32 ? 768 : 512;
+        const int64_t items = want / heads < 1 ? 1 : want / heads;
+        const int64_t cut = units < 1 ? 1 : units, each = tiles * a.requests;
+        // no row has more pieces than units, nor than the items if they are all its own
+        stride = cut < items ? cut : items;
+        stride = stride > kMaxChunks ? kMaxChunks : stride;
+        const int64_t grid = items + each;
+        p.few.items = (int)items;
+        p.few.grid = (int)(grid < each * cut ? grid : each * cut < 65535 ? each * cut : 65535);
+        p.few.grid = p.few.grid > 65535 ? 65535 : p.few.grid;
     }
     if (rows > kFewRows) {
         p.many.cols = rows <= 128 || a.type == BQ_F32 ? 128 : 256;
         const int64_t tiles = (rows + p.many.cols - 1) / p.many.cols;
         p.many.tiles = (int)(tiles < 32768 ? tiles : 32768);  // a grid dimension; the kernel walks on from there
-        split_keys(p.many, a, 512, 512);
+        // tiles that can have rows: no request has more than that, all together no more than the rows allow
+        const int64_t all = a.tokens * group / p.many.cols + a.requests, each = tiles * a.requests;
+        const int64_t busy = (each < all ? each : all) * heads, least = 512;
+        const int64_t steps = (a.max_keys + least - 1) / least;
+        int64_t chunks = 512 / busy;
+        chunks = chunks > steps ? steps : chunks;
+        chunks = chunks > kMaxChunks ? kMaxChunks : chunks < 1 ? 1 : chunks;
+        const int64_t per = steps < 1 ? 1 : (steps + chunks - 1) / chunks;
+        p.many.chunk = (int)(per * least);
+        p.many.chunks = (int)(steps < 1 ? 1 : (steps + per - 1) / per);
+        stride = stride > p.many.chunks ? stride : p.many.chunks;
     }
-    p.stride = p.few.chunks > p.many.chunks ? p.few.chunks : p.many.chunks;
+    p.stride = (int)stride;
     p.work_bytes = p.stride > 1 ? a.tokens * a.q_heads * p.stride * (4 * (int64_t)a.cache.dim + 8) : 0;
     return p;
 }
@@ -433,8 +559,9 @@ template <class OT, int D>
 static void join_type(const AttnArgs &g, hipStream_t st)
 {
     const bq_attn &a = g.a;
-    if (g.p.few.chunks > 1) {
-        const int64_t most = (int64_t)g.p.few.tiles * g.p.few.cols * a.cache.heads;
+    if (g.p.few.cols && g.p.stride > 1) {
+        const int64_t rows = (a.max_new < a.tokens ? a.max_new : a.tokens) * (a.q_heads / a.cache.heads);
+        const int64_t most = (rows < kFewRows ? rows : kFewRows) * a.cache.heads;
         hipLaunchKernelGGL((attn_join_few<OT, D>), dim3((unsigned)most, (unsigned)a.requests), dim3(256), 0, st, g);
     }
     if (g.p.many.chunks > 1) {
@@ -462,8 +589,8 @@ hipError_t launch_attn(const bq_attn &a, const AttnPlan &p, hipStream_t st)
         if (e != hipSuccess)
             return e;
     }
-    if (p.few.tiles) {
-        const dim3 grid((unsigned)a.cache.heads, (unsigned)(p.few.tiles * p.few.chunks), (unsigned)a.requests);
+    if (p.few.cols) {
+        const dim3 grid((unsigned)a.cache.heads, (unsigned)p.few.grid);
         if (f16)
             wide ? attn_dim<BQ_F16, 128>(g, grid, st) : attn_dim<BQ_F16, 64>(g, grid, st);
         else

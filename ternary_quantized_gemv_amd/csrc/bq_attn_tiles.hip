@@ -44,7 +44,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
     __shared__ v8 vs[2][D * 8];
 
     const bq_attn &a = g.a;
-    const AttnSplit &sp = g.p.many;
+    const auto &sp = g.p.many;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c32 = lane & 31, half = lane >> 5;
     const int b = blockIdx.z, kh = blockIdx.x;

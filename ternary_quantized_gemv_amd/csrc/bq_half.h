@@ -89,6 +89,15 @@ __device__ __forceinline__ void store8(T *p, const float (&v)[8])
     }
 }
 
+// Sixteen bytes as a vector of 16-bit values; ONCE: nothing reads them again,
+// so they need no place in the caches (non-temporal).
+template <class V, bool ONCE, class T>
+__device__ __forceinline__ V stream8(const T *p)
+{
+    const u32x4 *q = reinterpret_cast<const u32x4 *>(p);
+    return __builtin_bit_cast(V, ONCE ? __builtin_nontemporal_load(q) : *q);
+}
+
 // The maximum (or sum) over the two halves of a wavefront, and over the pairs
 // of 16-lane rows: lanes l, l ^ 32 and l, l ^ 16.
 template <class OP>

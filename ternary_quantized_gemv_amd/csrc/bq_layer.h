@@ -23,18 +23,25 @@ hipError_t launch_norm(int type, const NormArgs &a, int64_t rows, hipStream_t st
 
 hipError_t launch_append(const bq_append &a, hipStream_t st);
 
-// How bq_paged_attn splits its work (attn_plan), for each of its two kernels:
-// tiles of `cols` rows of one key head's queries, `tiles` of them at most per
-// request (0: not launched), each over `chunks` pieces of `chunk` keys that the
-// join adds up.
-struct AttnSplit {
-    int cols;
-    int tiles;
-    int chunks;
-    int chunk;
-};
+// How bq_paged_attn splits its work (attn_plan).  The kernel for few rows
+// (few.cols of one key head's queries a tile) cuts the keys of all requests
+// into about few.items pieces per key head, at most `stride` per row, on the
+// device, where the lengths are known; few.grid workgroups per key head walk
+// them.  The kernel for many rows (many.cols a tile, many.tiles of them at
+// most per request, 0: not launched) takes many.chunks pieces of many.chunk
+// keys.  The joins add the pieces up.
 struct AttnPlan {
-    AttnSplit few, many;
+    struct {
+        int cols;  // 0: not launched
+        int grid;
+        int items;
+    } few;
+    struct {
+        int cols;
+        int tiles;
+        int chunks;
+        int chunk;
+    } many;
     int stride;  // places per row for the pieces
     int64_t work_bytes;
 };

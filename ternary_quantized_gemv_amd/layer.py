@@ -10,6 +10,8 @@ call runs on the device of its tensors, whichever is current, and on `stream`
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct as _struct
 
 import torch
 
@@ -54,13 +56,29 @@ class bq_adapters(ctypes.Structure):
                 ("ld_y", _i64), ("out", _vp), ("ld_out", _i64), ("work", _vp), ("work_bytes", _i64)]
 
 
-for _name, _struct in (("bq_rmsnorm_q8", bq_norm), ("bq_kv_append", bq_append), ("bq_paged_attn", bq_attn),
-                       ("bq_adapters_add", bq_adapters)):
+def _format(struct) -> str:
+    """The struct module's format of a ctypes structure (nested ones flattened)."""
+    codes = {_i32: "i", _i64: "q", _f32: "f", ctypes.c_double: "d", _vp: "P"}
+    return "".join(codes[t] if t in codes else _format(t) for _, t in struct._fields_)
+
+
+class _Pack:
+    """Packs an argument block in one go: several times faster than filling the
+    ctypes structure, whose layout it has (native alignment, eight-byte end)."""
+
+    def __init__(self, struct):
+        self.pack = _struct.Struct("@" + _format(struct) + "0q").pack
+        assert len(self.pack(*[0] * len(_format(struct)))) == ctypes.sizeof(struct)
+
+
+_pack_norm, _pack_append, _pack_attn, _pack_adapters = (_Pack(k).pack for k in (bq_norm, bq_append, bq_attn, bq_adapters))
+
+for _name in ("bq_rmsnorm_q8", "bq_kv_append", "bq_paged_attn", "bq_adapters_add"):
     getattr(lib, _name).restype = ctypes.c_int
-    getattr(lib, _name).argtypes = [ctypes.POINTER(_struct), _vp]
-for _name, _struct in (("bq_paged_attn_work_bytes", bq_attn), ("bq_adapters_work_bytes", bq_adapters)):
+    getattr(lib, _name).argtypes = [_vp, _vp]
+for _name in ("bq_paged_attn_work_bytes", "bq_adapters_work_bytes"):
     getattr(lib, _name).restype = ctypes.c_int
-    getattr(lib, _name).argtypes = [ctypes.POINTER(_struct), ctypes.POINTER(_i64)]
+    getattr(lib, _name).argtypes = [_vp, _vp]
 
 
 # ------------------------------------------------------------------ checks
@@ -73,11 +91,11 @@ def _check(rc: int):
         raise BQError(rc, lib.bq_last_error().decode())
 
 
-def _first(fn: str, what: str, t):
-    """The tensor that says which device the call runs on."""
+def _first(fn: str, what: str, t) -> int:
+    """The index of the device that the call runs on, from the tensor that says so."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _refuse(fn, f"{what} must be a tensor on a ROCm device")
-    return t.device
+    return t.get_device()
 
 
 def _type(fn: str, what: str, t) -> int:
@@ -87,15 +105,21 @@ def _type(fn: str, what: str, t) -> int:
     return k
 
 
-def _rows(fn: str, what: str, t, dtype, device, shape):
+def _tensor(fn: str, what: str, t, dtype, dev: int):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _refuse(fn, f"{what} must be a tensor on device {dev}")
+    if t.dtype is not dtype:
+        _refuse(fn, f"{what} must be {dtype}, not {t.dtype}")
+
+
+def _rows(fn: str, what: str, t, dtype, dev: int, shape):
     """(pointer, elements between rows) of a tensor of this shape whose rows
     (all dimensions but the first) are contiguous; a single row may come
     without its first dimension."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        _refuse(fn, f"{what} must be a tensor on {device}")
-    if t.dtype is not dtype:
-        _refuse(fn, f"{what} must be {dtype}, not {t.dtype}")
+    _tensor(fn, what, t, dtype, dev)
     have, stride = t.shape, t.stride()
+    if have == shape and t.is_contiguous():
+        return t.data_ptr(), stride[0]
     if len(have) == len(shape) - 1 and shape[0] == 1:
         have, stride = (1, *have), (0, *stride)
     if tuple(have) != shape:
@@ -108,41 +132,40 @@ def _rows(fn: str, what: str, t, dtype, device, shape):
     return t.data_ptr(), stride[0]
 
 
-def _flat(fn: str, what: str, t, dtype, device, n: int) -> int:
+def _flat(fn: str, what: str, t, dtype, dev: int, n: int) -> int:
     """Pointer of a contiguous tensor of n values."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        _refuse(fn, f"{what} must be a tensor on {device}")
-    if t.dtype is not dtype:
-        _refuse(fn, f"{what} must be {dtype}, not {t.dtype}")
+    _tensor(fn, what, t, dtype, dev)
     if t.numel() != n or not t.is_contiguous():
         _refuse(fn, f"{what} must be contiguous with {n} values, has shape {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _run(call, args, device, stream):
-    if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
-    else:
-        stream = getattr(stream, "cuda_stream", stream)
-    if device.index == torch.cuda.current_device():
+# the stream and device lookups without the objects that torch.cuda makes of them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _run(call, args: bytes, dev: int, stream):
+    stream = _raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
+    if dev == _current_device():
         _check(call(args, stream))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             _check(call(args, stream))
 
 
-def _scratch(fn: str, work, need: int, device, stream):
+def _scratch(fn: str, work, need: int, dev: int, stream):
     """The caller's scratch tensor, or one of this call: allocated on the
     stream that the call runs on, so that the allocator reuses it in order."""
     if work is None:
         if stream is None or not need:
-            return torch.empty(need, dtype=torch.uint8, device=device)
+            return torch.empty(need, dtype=torch.uint8, device=dev)
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream, device=device)
+            stream = torch.cuda.ExternalStream(stream, device=dev)
         with torch.cuda.stream(stream):
-            return torch.empty(need, dtype=torch.uint8, device=device)
-    if not isinstance(work, torch.Tensor) or work.device != device or not work.is_contiguous():
-        _refuse(fn, f"work must be a contiguous tensor on {device}")
+            return torch.empty(need, dtype=torch.uint8, device=dev)
+    if not isinstance(work, torch.Tensor) or work.get_device() != dev or not work.is_contiguous():
+        _refuse(fn, f"work must be a contiguous tensor on device {dev}")
     return work
 
 
@@ -155,18 +178,21 @@ def bq_rmsnorm_q8(x, w, eps: float, qa: int, q, d, res=None, h=None, y=None, f16
     h receives x + res, y the normed rows; either may be x or res."""
     fn = "bq_rmsnorm_q8"
     dev = _first(fn, "x", x)
-    kind, dt = _type(fn, "x", x), x.dtype
-    if x.dim() not in (1, 2):
+    kind, dt, shape = _type(fn, "x", x), x.dtype, x.shape
+    if len(shape) == 2:
+        T, n = shape
+    elif len(shape) == 1:
+        T, n = 1, shape[0]
+    else:
         _refuse(fn, "x must be [tokens, n] or [n]")
-    n = x.shape[-1]
-    T = x.shape[0] if x.dim() == 2 else 1
     shape = (T, n)
-    a = bq_norm(kind, qa, int(f16_scale), 0, eps, T, n, *_rows(fn, "x", x, dt, dev, shape),
-                *((None, 0) if res is None else _rows(fn, "res", res, dt, dev, shape)),
-                *((None, 0) if h is None else _rows(fn, "h", h, dt, dev, shape)), _flat(fn, "w", w, dt, dev, n),
-                *_rows(fn, "q", q, torch.int8, dev, shape),
-                *_rows(fn, "d", d, torch.float32, dev, (T, n // qa if qa > 0 else 0)),
-                *((None, 0) if y is None else _rows(fn, "y", y, dt, dev, shape)))
+    none = (0, 0)
+    a = _pack_norm(kind, qa, int(f16_scale), 0, eps, T, n, *_rows(fn, "x", x, dt, dev, shape),
+                   *(none if res is None else _rows(fn, "res", res, dt, dev, shape)),
+                   *(none if h is None else _rows(fn, "h", h, dt, dev, shape)), _flat(fn, "w", w, dt, dev, n),
+                   *_rows(fn, "q", q, torch.int8, dev, shape),
+                   *_rows(fn, "d", d, torch.float32, dev, (T, n // qa if qa > 0 else 0)),
+                   *(none if y is None else _rows(fn, "y", y, dt, dev, shape)))
     _run(lib.bq_rmsnorm_q8, a, dev, stream)
 
 
@@ -176,17 +202,16 @@ class KVCache:
 
     def __init__(self, k, v):
         fn = "KVCache"
-        dev = _first(fn, "k", k)
+        self.dev = dev = _first(fn, "k", k)
         if k.dim() != 4:
             _refuse(fn, "k must be [pages, heads, page, dim]")
-        pages, heads, page, dim = k.shape
-        kp = _flat(fn, "k", k, k.dtype, dev, k.numel())
-        vp = _flat(fn, "v", v, k.dtype, dev, k.numel())
-        if v.shape != (pages, heads, dim, page):
-            _refuse(fn, f"v has shape {tuple(v.shape)}, needs {(pages, heads, dim, page)}")
-        self.k, self.v, self.device = k, v, dev
-        self.pages, self.heads, self.page, self.dim = pages, heads, page, dim
-        self.c = bq_kv_cache(_type(fn, "k", k), heads, dim, page, pages, kp, vp)
+        self.pages, self.heads, self.page, self.dim = pages, heads, page, dim = k.shape
+        kp = _rows(fn, "k", k, k.dtype, dev, (pages, heads, page, dim))[0]
+        vp = _rows(fn, "v", v, k.dtype, dev, (pages, heads, dim, page))[0]
+        if not k.is_contiguous() or not v.is_contiguous():
+            _refuse(fn, "k and v must be contiguous")
+        self.k, self.v = k, v
+        self.c = (_type(fn, "k", k), heads, dim, page, pages, kp, vp)
 
     @classmethod
     def empty(cls, pages: int, heads: int, dim: int, page: int = 64, dtype=torch.bfloat16, device="cuda"):
@@ -202,35 +227,42 @@ def bq_kv_append(cache: KVCache, k, v, pos, slot, freq, q=None, q_out=None, q_no
     (page * page size + offset) or -1; freq: float32 [rot / 2]; q_norm,
     k_norm: float32 [dim].  The rotated queries go to q_out (q itself allowed)."""
     fn = "bq_kv_append"
-    dev, c = cache.device, cache
+    dev, c = cache.dev, cache
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         _refuse(fn, "k must be [tokens, heads, dim]")
     dt, T = k.dtype, k.shape[0]
     shape = (T, c.heads, c.dim)
     kind = _type(fn, "k", k)
     Hq = 0
-    qp = qo = (None, 0)
+    qp = qo = (0, 0)
     out_kind = kind
     if (q is None) != (q_out is None):
         _refuse(fn, "q and q_out come together")
     if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
-            _refuse(fn, "q must be [tokens, q_heads, dim]")
+        if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(q_out, torch.Tensor):
+            _refuse(fn, "q and q_out must be [tokens, q_heads, dim]")
         Hq = q.shape[1]
         qp = _rows(fn, "q", q, dt, dev, (T, Hq, c.dim))
-        if not isinstance(q_out, torch.Tensor):
-            _refuse(fn, "q_out must be a tensor")
         out_kind = _type(fn, "q_out", q_out)
         qo = _rows(fn, "q_out", q_out, q_out.dtype, dev, (T, Hq, c.dim))
     if not isinstance(freq, torch.Tensor):
         _refuse(fn, "freq must be a tensor")
-    a = bq_append(c.c, kind, out_kind, Hq, 2 * freq.numel(), eps, 0, T, *qp, *_rows(fn, "k", k, dt, dev, shape),
-                  *_rows(fn, "v", v, dt, dev, shape), *qo, _flat(fn, "pos", pos, torch.int32, dev, T),
-                  _flat(fn, "slot", slot, torch.int64, dev, T),
-                  _flat(fn, "freq", freq, torch.float32, dev, freq.numel()),
-                  None if q_norm is None else _flat(fn, "q_norm", q_norm, torch.float32, dev, c.dim),
-                  None if k_norm is None else _flat(fn, "k_norm", k_norm, torch.float32, dev, c.dim))
+    half = freq.numel()
+    a = _pack_append(*c.c, kind, out_kind, Hq, 2 * half, eps, 0, T, *qp, *_rows(fn, "k", k, dt, dev, shape),
+                     *_rows(fn, "v", v, dt, dev, shape), *qo, _flat(fn, "pos", pos, torch.int32, dev, T),
+                     _flat(fn, "slot", slot, torch.int64, dev, T), _flat(fn, "freq", freq, torch.float32, dev, half),
+                     0 if q_norm is None else _flat(fn, "q_norm", q_norm, torch.float32, dev, c.dim),
+                     0 if k_norm is None else _flat(fn, "k_norm", k_norm, torch.float32, dev, c.dim))
     _run(lib.bq_kv_append, a, dev, stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def _attn_work(cache_sizes, kind, q_heads, requests, tokens, max_new, max_keys) -> int:
+    need = _i64()
+    _check(lib.bq_paged_attn_work_bytes(
+        _pack_attn(*cache_sizes, 0, 0, kind, q_heads, requests, 1, 1, tokens, max_new, max_keys, *[0] * 7, 0.0, *[0] * 3),
+        ctypes.byref(need)))
+    return need.value
 
 
 def bq_paged_attn(cache: KVCache, q, cu, lens, table, scale: float, max_new: int, max_keys: int, out, work=None,
@@ -242,39 +274,31 @@ def bq_paged_attn(cache: KVCache, q, cu, lens, table, scale: float, max_new: int
     least bq_paged_attn_work_bytes(...) bytes, by default a tensor of the call's
     own (calls that may run at the same time must not share one)."""
     fn = "bq_paged_attn"
-    a, dev = _attn_args(fn, cache, q, cu, lens, table, scale, max_new, max_keys, out)
-    need = _i64()
-    _check(lib.bq_paged_attn_work_bytes(a, need))
-    work = _scratch(fn, work, need.value, dev, stream)
-    a.work, a.work_bytes = work.data_ptr(), work.numel() * work.element_size()
-    _run(lib.bq_paged_attn, a, dev, stream)
-
-
-def _attn_args(fn, cache, q, cu, lens, table, scale, max_new, max_keys, out):
-    dev, c = cache.device, cache
+    dev, c = cache.dev, cache
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         _refuse(fn, "q must be [tokens, q_heads, dim]")
     if not isinstance(lens, torch.Tensor) or lens.dim() != 1:
         _refuse(fn, "lens must be [requests]")
-    dt, B = q.dtype, lens.shape[0]
-    T, Hq, _ = shape = (q.shape[0], q.shape[1], c.dim)
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         _refuse(fn, "table must be [requests, pages of a request]")
-    tp, ld_table = _rows(fn, "table", table, torch.int32, dev, (B, table.shape[1]))
-    return bq_attn(c.c, _type(fn, "q", q), Hq, B, table.shape[1], ld_table, T, max_new, max_keys,
+    dt, kind, B = q.dtype, _type(fn, "q", q), lens.shape[0]
+    shape = (q.shape[0], q.shape[1], c.dim)
+    cols = table.shape[1]
+    tp, ld_table = _rows(fn, "table", table, torch.int32, dev, (B, cols))
+    need = _attn_work(c.c[:5], kind, shape[1], B, shape[0], max_new, max_keys)
+    work = _scratch(fn, work, need, dev, stream)
+    a = _pack_attn(*c.c, kind, shape[1], B, cols, ld_table, shape[0], max_new, max_keys,
                    *_rows(fn, "q", q, dt, dev, shape), *_rows(fn, "out", out, dt, dev, shape),
-                   _flat(fn, "cu", cu, torch.int32, dev, B + 1), _flat(fn, "lens", lens, torch.int32, dev, B), tp,
-                   scale, 0, None, 0), dev
+                   _flat(fn, "cu", cu, torch.int32, dev, B + 1), _flat(fn, "lens", lens, torch.int32, dev, B), tp, scale,
+                   0, work.data_ptr(), work.nbytes)
+    _run(lib.bq_paged_attn, a, dev, stream)
 
 
-def bq_paged_attn_work_bytes(cache: KVCache, tokens: int, q_heads: int, requests: int, max_new: int,
-                             max_keys: int) -> int:
+def bq_paged_attn_work_bytes(cache: KVCache, tokens: int, q_heads: int, requests: int, max_new: int, max_keys: int,
+                             q_type=torch.float32) -> int:
     """Bytes of scratch that bq_paged_attn needs for these sizes (tables of
     any width)."""
-    a = bq_attn(cache.c, BQ_F32, q_heads, requests, 1, 1, tokens, max_new, max_keys)
-    need = _i64()
-    _check(lib.bq_paged_attn_work_bytes(a, need))
-    return need.value
+    return _attn_work(cache.c[:5], TYPES[q_type], q_heads, requests, tokens, max_new, max_keys)
 
 
 class Adapters:
@@ -283,18 +307,26 @@ class Adapters:
 
     def __init__(self, a, b, gain):
         fn = "Adapters"
-        dev = _first(fn, "a", a)
+        self.dev = dev = _first(fn, "a", a)
         if a.dim() != 3 or not isinstance(b, torch.Tensor) or b.dim() != 3:
             _refuse(fn, "a must be [count, rank, n] and b [count, rows, rank]")
-        self.count, self.rank, self.n = a.shape
-        self.rows = b.shape[1]
-        self._a = _flat(fn, "a", a, a.dtype, dev, a.numel())
-        if b.shape != (self.count, self.rows, self.rank):
-            _refuse(fn, f"b has shape {tuple(b.shape)}, needs {(self.count, self.rows, self.rank)}")
-        self._b = _flat(fn, "b", b, a.dtype, dev, b.numel())
-        self._gain = _flat(fn, "gain", gain, torch.float32, dev, self.count)
-        self.a, self.b, self.gain, self.device = a, b, gain, dev
+        self.count, self.rank, self.n = count, rank, n = a.shape
+        self.rows = rows = b.shape[1]
+        ap = _rows(fn, "a", a, a.dtype, dev, (count, rank, n))[0]
+        bp = _rows(fn, "b", b, a.dtype, dev, (count, rows, rank))[0]
+        if not a.is_contiguous() or not b.is_contiguous():
+            _refuse(fn, "a and b must be contiguous")
+        self.pointers = (ap, bp, _flat(fn, "gain", gain, torch.float32, dev, count))
+        self.a, self.b, self.gain = a, b, gain
         self.type = _type(fn, "a", a)
+
+
+@functools.lru_cache(maxsize=1024)
+def _adapters_work(kind, x_kind, rank, count, requests, n, rows, tokens, max_new) -> int:
+    need = _i64()
+    _check(lib.bq_adapters_work_bytes(
+        _pack_adapters(kind, x_kind, rank, count, requests, 0, n, rows, tokens, max_new, *[0] * 13), ctypes.byref(need)))
+    return need.value
 
 
 def bq_adapters_add(adapters: Adapters, x, cu, ids, max_new: int, y, out=None, work=None, stream=None) -> None:
@@ -305,28 +337,23 @@ def bq_adapters_add(adapters: Adapters, x, cu, ids, max_new: int, y, out=None, w
     of at least bq_adapters_work_bytes(...) bytes, by default a tensor of the
     call's own."""
     fn = "bq_adapters_add"
-    p, dev = adapters, adapters.device
+    p, dev = adapters, adapters.dev
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         _refuse(fn, "x must be [tokens, n]")
     if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
         _refuse(fn, "ids must be [requests]")
-    T, B = x.shape[0], ids.shape[0]
+    T, B, kind = x.shape[0], ids.shape[0], _type(fn, "x", x)
+    sizes = (p.type, kind, p.rank, p.count, B)
+    work = _scratch(fn, work, _adapters_work(*sizes, p.n, p.rows, T, max_new), dev, stream)
     yp = _rows(fn, "y", y, torch.float32, dev, (T, p.rows))
-    a = bq_adapters(p.type, _type(fn, "x", x), p.rank, p.count, B, 0, p.n, p.rows, T, max_new, p._a, p._b, p._gain,
-                    *_rows(fn, "x", x, x.dtype, dev, (T, p.n)), _flat(fn, "cu", cu, torch.int32, dev, B + 1),
-                    _flat(fn, "ids", ids, torch.int32, dev, B), *yp,
-                    *(yp if out is None else _rows(fn, "out", out, torch.float32, dev, (T, p.rows))), None, 0)
-    need = _i64()
-    _check(lib.bq_adapters_work_bytes(a, need))
-    work = _scratch(fn, work, need.value, dev, stream)
-    a.work, a.work_bytes = work.data_ptr(), work.numel() * work.element_size()
+    a = _pack_adapters(*sizes, 0, p.n, p.rows, T, max_new, *p.pointers, *_rows(fn, "x", x, x.dtype, dev, (T, p.n)),
+                       _flat(fn, "cu", cu, torch.int32, dev, B + 1), _flat(fn, "ids", ids, torch.int32, dev, B), *yp,
+                       *(yp if out is None else _rows(fn, "out", out, torch.float32, dev, (T, p.rows))), work.data_ptr(),
+                       work.nbytes)
     _run(lib.bq_adapters_add, a, dev, stream)
 
 
 def bq_adapters_work_bytes(adapters: Adapters, tokens: int, requests: int, max_new: int, x_type=torch.float32) -> int:
     """Bytes of scratch that bq_adapters_add needs for these sizes."""
     p = adapters
-    a = bq_adapters(p.type, TYPES[x_type], p.rank, p.count, requests, 0, p.n, p.rows, tokens, max_new)
-    need = _i64()
-    _check(lib.bq_adapters_work_bytes(a, need))
-    return need.value
+    return _adapters_work(p.type, TYPES[x_type], p.rank, p.count, requests, p.n, p.rows, tokens, max_new)

@@ -49,7 +49,7 @@ def adapters(**k):
 
 
 def rc_of(fn, a):
-    return getattr(bq.lib, fn)(a, None)
+    return getattr(bq.lib, fn)(ctypes.byref(a), None)
 
 
 CASES = [
@@ -119,20 +119,20 @@ def test_norm_eps_needed_with_weights_only():
 
 def test_scratch_sizes():
     need = ctypes.c_int64(-1)
-    assert bq.lib.bq_paged_attn_work_bytes(attn(), need) == bq.BQ_OK and need.value >= 0
+    assert bq.lib.bq_paged_attn_work_bytes(ctypes.byref(attn()), ctypes.byref(need)) == bq.BQ_OK and need.value >= 0
     few = need.value
     # one short row over many keys is split: partial sums of 64 values, a maximum and a sum per row and piece
-    assert bq.lib.bq_paged_attn_work_bytes(attn(tokens=1, requests=1, max_new=1, max_keys=100000), need) == bq.BQ_OK
+    assert bq.lib.bq_paged_attn_work_bytes(ctypes.byref(attn(tokens=1, requests=1, max_new=1, max_keys=100000)), ctypes.byref(need)) == bq.BQ_OK
     assert need.value > 4 * (4 * 64 + 8) and need.value % (4 * (4 * 64 + 8)) == 0
     a = attn(tokens=1, requests=1, max_new=1, max_keys=100000, work=None)
     assert rc_of("bq_paged_attn", a) == bq.BQ_EARG and "work" in bq.bq_last_error()
     a = attn(tokens=1, requests=1, max_new=1, max_keys=100000, work_bytes=need.value - 1)
     assert rc_of("bq_paged_attn", a) == bq.BQ_EARG and "work" in bq.bq_last_error()
-    assert bq.lib.bq_paged_attn_work_bytes(attn(tokens=0), need) == bq.BQ_OK and need.value == 0
-    assert bq.lib.bq_paged_attn_work_bytes(attn(), None) == bq.BQ_EARG and few >= 0
-    assert bq.lib.bq_adapters_work_bytes(adapters(), need) == bq.BQ_OK and need.value > 0
-    assert bq.lib.bq_adapters_work_bytes(adapters(rank=12), need) == bq.BQ_EARG
-    assert bq.lib.bq_adapters_work_bytes(adapters(), None) == bq.BQ_EARG
+    assert bq.lib.bq_paged_attn_work_bytes(ctypes.byref(attn(tokens=0)), ctypes.byref(need)) == bq.BQ_OK and need.value == 0
+    assert bq.lib.bq_paged_attn_work_bytes(ctypes.byref(attn()), None) == bq.BQ_EARG and few >= 0
+    assert bq.lib.bq_adapters_work_bytes(ctypes.byref(adapters()), ctypes.byref(need)) == bq.BQ_OK and need.value > 0
+    assert bq.lib.bq_adapters_work_bytes(ctypes.byref(adapters(rank=12)), ctypes.byref(need)) == bq.BQ_EARG
+    assert bq.lib.bq_adapters_work_bytes(ctypes.byref(adapters()), None) == bq.BQ_EARG
 
 
 def test_binding_refuses_host_tensors():
