@@ -59,6 +59,47 @@ __device__ __forceinline__ int page_at(const AttnArgs &g, const int32_t *table, 
     return (unsigned)p < (unsigned)g.a.cache.pages ? p : -1;
 }
 
+// Eight values in NP parts of type T: rounded, then the rest rounded.  Three
+// parts of bf16 cut an f32's 24 bits into eights, exactly and without
+// conversions (512 f32 rows over 30011 keys: 755 -> 717 us).
+template <class T, int NP> struct Split {
+    typedef T t8 __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ void parts(const float (&x)[8], t8 (&f)[NP])
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float rest = x[e];
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                f[p][e] = (T)rest;
+                rest -= (float)f[p][e];
+            }
+        }
+    }
+};
+__device__ __forceinline__ uint32_t upper_halves(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); }
+template <> struct Split<__bf16, 3> {
+    static __device__ __forceinline__ void parts(const float (&x)[8], bf16x8 (&f)[3])
+    {
+        float rest[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            rest[e] = x[e];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            u32x4 w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = upper_halves(__builtin_bit_cast(uint32_t, rest[2 * i]), __builtin_bit_cast(uint32_t, rest[2 * i + 1]));
+            f[p] = __builtin_bit_cast(bf16x8, w);
+            if (p < 2)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    rest[e] -= __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, rest[e]) & 0xFFFF0000u);
+        }
+    }
+};
+
 // One column's query fragments: element e of fragment j is q[at + step j + e].
 // Returns the factor from products with the fragments to log2 units, never
 // negative: a negative scale turns the sign of q instead, so that the largest
@@ -104,16 +145,13 @@ __device__ __forceinline__ float load_query(const bq_attn &a, int64_t at, int st
             factor = __builtin_ldexpf(factor, ex - 14);
         }
 #pragma unroll
-        for (int j = 0; j < N; ++j)
+        for (int j = 0; j < N; ++j) {
+            v8 part[NP];
+            Split<T, NP>::parts(x[j], part);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float rest = x[j][e];
-#pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    f[p][j][e] = (T)rest;
-                    rest -= (float)f[p][j][e];
-                }
-            }
+            for (int p = 0; p < NP; ++p)
+                f[p][j] = part[p];
+        }
     }
     return factor;
 }

@@ -290,14 +290,10 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 && !F32 ? 3 : 2) void attn
                 v8 pf[NP];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float rest = __builtin_amdgcn_exp2f(__builtin_fmaf(w[e], factor, shift));
-                    l[t] += rest;
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        pf[p][e] = (T)rest;
-                        rest -= (float)pf[p][e];
-                    }
+                    w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(w[e], factor, shift));
+                    l[t] += w[e];
                 }
+                Split<T, NP>::parts(w, pf);
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -525,7 +521,7 @@ AttnPlan attn_plan(const bq_attn &a)
         const int64_t all = a.tokens * group / p.many.cols + a.requests, each = tiles * a.requests;
         const int64_t busy = (each < all ? each : all) * heads, least = 512;
         const int64_t steps = (a.max_keys + least - 1) / least;
-        int64_t chunks = 512 / busy;
+        int64_t chunks = 256 / busy;  // one filling of the compute units
         chunks = chunks > steps ? steps : chunks;
         chunks = chunks > kMaxChunks ? kMaxChunks : chunks < 1 ? 1 : chunks;
         const int64_t per = steps < 1 ? 1 : (steps + chunks - 1) / chunks;

@@ -36,6 +36,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
     constexpr float UP = CT == BQ_F16 ? 6.0f : 0.0f;
     constexpr int THREADS = 64 * WAVES, ROWS = 32 * WAVES;
     constexpr int DJ = D / 16, DT = D / 32, KC = D / 8;  // steps and tiles of D; 16-byte pieces of a key
+    // the wavefront of a SIMD that has products to issue goes first, the other's exponentials fill the gaps
+    // (+2%; 5% slower where the products are three times as many, or half as long)
+    constexpr bool FIRST = !F32 && D == 128;
     constexpr int BLOCKS = kTileKeys / 16;               // of 16 keys: one page each
     constexpr int KL = kTileKeys * KC / THREADS, VL = D * 8 / THREADS;  // pieces a thread stages
     constexpr int KROWS = THREADS / KC, VROWS = THREADS / 8;            // rows that one piece of each thread covers
@@ -168,6 +171,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
                 for (int e = 0; e < 16; ++e)
                     s[e] = 0.0f;
                 const int krow = 32 * h + c32;
+                if (FIRST)
+                    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int j = 0; j < DJ; ++j) {
                     const v8 kf = ks[buf][krow * KC + ((2 * j + half) ^ (krow & 7))];
@@ -175,6 +180,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
                     for (int p = NP - 1; p >= 0; --p)
                         s = Num<CT>::mfma32(kf, qf[p][j], s);
                 }
+                if (FIRST)
+                    __builtin_amdgcn_s_setprio(0);
                 // ---- weights
                 float factor = qs, top = kNone;
                 if (!whole) {
@@ -203,17 +210,23 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
                 float sum = 0.0f;
                 v8 pf[NP][2];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float rest = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], factor, shift));
-                    sum += rest;
+                for (int k = 0; k < 2; ++k) {
+                    float w[8];
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        pf[p][e >> 3][e & 7] = (T)rest;
-                        rest -= (float)pf[p][e >> 3][e & 7];
+                    for (int e = 0; e < 8; ++e) {
+                        w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * k + e], factor, shift));
+                        sum += w[e];
                     }
+                    v8 part[NP];
+                    Split<T, NP>::parts(w, part);
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        pf[p][k] = part[p];
                 }
                 l += sum;
                 // ---- values
+                if (FIRST)
+                    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
                     const int row = 32 * d + c32;
@@ -225,6 +238,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
                             o[d] = Num<CT>::mfma32(vf, pf[p][k], o[d]);
                     }
                 }
+                if (FIRST)
+                    __builtin_amdgcn_s_setprio(0);
             }
             if (next < end) {
                 stage(next, buf ^ 1);
