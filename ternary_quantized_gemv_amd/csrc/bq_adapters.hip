@@ -1,88 +1,403 @@
 // bq_adapters.hip -- low-rank updates of many requests beside a shared
 // projection (bq_adapters_add): out = y + gain B (A x), row by row, each
 // request with its own A (rank x n) and B (rows x rank).
-#include "bq_half.h"
-#include "bq_layer.h"
+//
+// Two launches: u = gain A x, split along n where the requests are few (pieces
+// in the scratch, added up by the second launch in a fixed order), then out = y +
+// B u.  Both are v_mfma_f32_16x16x32 products with the adapter's rows along the
+// result's rows and up to 16 tokens of one request along its columns; a decode
+// step uses one column, which costs nothing: the adapters' weights bound it
+// (read once a request), or for prompts x, y and out.
+//
+// f32 values (x, and u) enter as three bf16 parts that hold their 24 bits
+// exactly; f16 weights beside them as two (8 and 3 bits, exact), all products
+// but the smallest (2^-24 of the largest, at most) on the matrix cores.
+#include "bq_attn.h"
 
 namespace bq {
 
-// u[t][r] = gain A[r] . x[t]: one workgroup per row, a wavefront per rank.
-template <class T, class X>
-__global__ __launch_bounds__(256) void adapters_down(const bq_adapters a)
+constexpr int kDownStep = 128;    // values of n that a workgroup's four wavefronts take at a time
+constexpr int kMaxPieces = 16;    // of n
+constexpr int kUpRows = 256;      // rows of B per workgroup
+
+struct AdapterArgs {
+    bq_adapters a;
+    int pieces;       // of n
+    int piece;        // values of n in each
+    int down_items;   // items along the grid, 16 NT tokens each
+    int up_items;
+    int direct;       // item i is request i (few tokens each), else the items of all requests are counted through
+};
+
+// Item `item` of 16 NT tokens each: request b, its rows and where they start.
+// With `direct` a request is one item, which walks its rows.
+template <int TOKENS>
+__device__ __forceinline__ bool adapter_item(const AdapterArgs &g, int item, int &b, int &first, int &end)
 {
-    const int64_t t = blockIdx.x;
-    const int b = request_of(a.cu, a.requests, (int)t);
-    const int id = b < 0 ? -1 : a.ids[b];
-    if ((unsigned)id >= (unsigned)a.count)
-        return;
+    const bq_adapters &a = g.a;
+    auto rows_of = [&](int i, int &lo) {
+        lo = a.cu[i];
+        int hi = a.cu[i + 1];
+        hi = hi > a.tokens ? (int)a.tokens : hi;
+        return lo < 0 || hi < lo ? 0 : hi - lo;
+    };
+    if (g.direct) {
+        if (item >= a.requests)
+            return false;
+        b = item;
+        first = uniform_word(a.cu + b);
+        end = uniform_word(a.cu + b + 1);
+        end = end > a.tokens ? (int)a.tokens : end;
+        if (first < 0)
+            end = first = 0;
+        return true;
+    }
     const int lane = threadIdx.x & 63;
-    const X *x = static_cast<const X *>(a.x) + t * a.ld_x;
-    for (int r = threadIdx.x >> 6; r < a.rank; r += 4) {
-        const T *w = static_cast<const T *>(a.a) + ((int64_t)id * a.rank + r) * a.n;
-        float sum = 0.0f;
-        for (int64_t i = 8 * lane; i < a.n; i += 512) {
-            float u[8], v[8];
-            load8(w + i, u);
-            load8(x + i, v);
+    int before = 0;
+    for (int base = 0; base < a.requests; base += 64) {
+        int lo = 0, n = 0;
+        if (base + lane < a.requests)
+            n = rows_of(base + lane, lo);
+        const int mine = (n + TOKENS - 1) / TOKENS;
+        int upto = mine;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sum = __builtin_fmaf(u[e], v[e], sum);
+        for (int off = 1; off < 64; off <<= 1) {
+            const int x = __shfl_up(upto, off, 64);
+            upto += lane >= off ? x : 0;
         }
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1)
-            sum += __shfl_xor(sum, off, 64);
-        if (lane == 0)
-            static_cast<float *>(a.work)[t * a.rank + r] = sum * a.gain[id];
+        const unsigned long long has = __ballot(item - before < upto);
+        if (has) {
+            const int at = __builtin_ctzll(has);
+            b = base + at;
+            const int within = item - before - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at));
+            const int l = __builtin_amdgcn_readlane(lo, at), m = __builtin_amdgcn_readlane(n, at);
+            first = l + within * TOKENS;
+            end = min(first + TOKENS, l + m);
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
     }
+    return false;
 }
 
-// out[t][row] = y[t][row] + B[row] . u[t]: one thread per row of B.
-template <class T>
-__global__ __launch_bounds__(256) void adapters_up(const bq_adapters a)
+// c += W X^T for 32 values of k: weights w (16 bits), values x as f32 or of the weights' type.
+template <class T, class X> struct Step;
+template <class T> struct Step<T, T> {
+    typedef T t8 __attribute__((ext_vector_type(8)));
+    typedef t8 raw;
+    t8 x;
+    __device__ __forceinline__ void set(raw v) { x = v; }
+    __device__ __forceinline__ f32x4 add(t8 w, f32x4 c) const
+    {
+        return Num<sizeof(T) == 2 && __is_same(T, _Float16) ? BQ_F16 : BQ_BF16>::mfma16(w, x, c);
+    }
+};
+template <class T> struct Step<T, float> {
+    typedef T t8 __attribute__((ext_vector_type(8)));
+    typedef float raw __attribute__((ext_vector_type(8), aligned(16)));
+    bf16x8 x[3];
+    __device__ __forceinline__ void set(raw r)
+    {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = r[e];
+        Split<__bf16, 3>::parts(v, x);
+    }
+    __device__ __forceinline__ f32x4 add(t8 w, f32x4 c) const
+    {
+        typedef Num<BQ_BF16> N;
+        if constexpr (__is_same(T, __bf16)) {
+            c = N::mfma16(w, x[2], c);
+            c = N::mfma16(w, x[1], c);
+            return N::mfma16(w, x[0], c);
+        } else {
+            // an f16's 11 bits as 8 and 3
+            u32x4 hi, lo;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t p = __builtin_bit_cast(uint32_t, (float)w[2 * i]), q = __builtin_bit_cast(uint32_t, (float)w[2 * i + 1]);
+                const float pr = (float)w[2 * i] - __builtin_bit_cast(float, p & 0xFFFF0000u);
+                const float qr = (float)w[2 * i + 1] - __builtin_bit_cast(float, q & 0xFFFF0000u);
+                hi[i] = upper_halves(p, q);
+                lo[i] = upper_halves(__builtin_bit_cast(uint32_t, pr), __builtin_bit_cast(uint32_t, qr));
+            }
+            const bf16x8 h = __builtin_bit_cast(bf16x8, hi), l = __builtin_bit_cast(bf16x8, lo);
+            c = N::mfma16(h, x[2], c);
+            c = N::mfma16(l, x[1], c);
+            c = N::mfma16(h, x[1], c);
+            c = N::mfma16(l, x[0], c);
+            return N::mfma16(h, x[0], c);
+        }
+    }
+};
+
+// u[piece][t][r] = gain A[r] . x[t] over a piece of n: ranks along the result's
+// rows (RT tiles of 16), tokens along its columns (NT tiles).
+template <class T, class X, int RT, int NT>
+__global__ __launch_bounds__(256) void adapters_down(const AdapterArgs g)
 {
-    const int64_t t = blockIdx.x;
-    const int b = request_of(a.cu, a.requests, (int)t);
-    if (b < 0)
-        return;
-    const int id = a.ids[b];
-    const int64_t row = (int64_t)blockIdx.y * 256 + threadIdx.x;
-    if (row >= a.rows)
-        return;
-    float sum = a.y[t * a.ld_y + row];
-    if ((unsigned)id < (unsigned)a.count) {
-        const T *w = static_cast<const T *>(a.b) + ((int64_t)id * a.rows + row) * a.rank;
-        const float *u = static_cast<const float *>(a.work) + t * a.rank;
-        float add = 0.0f;
-        for (int r = 0; r < a.rank; r += 8) {
-            float v[8];
-            load8(w + r, v);
+    typedef T t8 __attribute__((ext_vector_type(8)));
+    constexpr int U = RT * NT <= 4 ? 4 : 2;
+    __shared__ float red[4][NT][RT][16][17];
+    const bq_adapters &a = g.a;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, q4 = lane >> 4;
+    const int piece = blockIdx.x % g.pieces;
+    const int64_t from = (int64_t)piece * g.piece, to = min(from + g.piece, a.n);
+    int b, first, end;
+    for (int item = blockIdx.x / g.pieces; adapter_item<16 * NT>(g, item, b, first, end); item += gridDim.x / g.pieces) {
+        const int id = uniform_word(a.ids + b);
+        if ((unsigned)id >= (unsigned)a.count)
+            continue;
+        const float gain = a.gain[id];
+        const T *w[RT];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                add = __builtin_fmaf(v[e], u[r + e], add);
+        for (int r = 0; r < RT; ++r)
+            w[r] = static_cast<const T *>(a.a) + ((int64_t)id * a.rank + min(16 * r + c16, a.rank - 1)) * a.n + 8 * q4;
+        for (int t0 = first; t0 < end; t0 += 16 * NT) {
+            f32x4 acc[NT][RT];
+            const X *x[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                x[t] = static_cast<const X *>(a.x) + (int64_t)min(t0 + 16 * t + c16, end - 1) * a.ld_x + 8 * q4;
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                    acc[t][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+            for (int64_t i0 = from + 32 * wave; i0 < to; i0 += U * kDownStep) {
+                // the loads of U steps, then their products
+                typename Step<T, X>::raw x8[U][NT];
+                t8 v[U][RT];
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int64_t i = i0 + j * kDownStep;
+                    const bool in = i + 8 * q4 < to;  // n is a multiple of 8: the last lanes may have none
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+                        v[j][r] = in ? *reinterpret_cast<const t8 *>(w[r] + i) : t8{};
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        x8[j][t] = in ? *reinterpret_cast<const typename Step<T, X>::raw *>(x[t] + i) : typename Step<T, X>::raw{};
+                }
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        Step<T, X> s;
+                        s.set(x8[j][t]);
+#pragma unroll
+                        for (int r = 0; r < RT; ++r)
+                            acc[t][r] = s.add(v[j][r], acc[t][r]);
+                    }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        red[wave][t][r][c16][4 * q4 + e] = acc[t][r][e];
+            __syncthreads();
+            for (int u = threadIdx.x; u < NT * 16 * RT * 16; u += 256) {
+                const int r = u % (16 * RT), t = u / (16 * RT);
+                if (r < a.rank && t0 + t < end) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sum += red[k][t >> 4][r >> 4][t & 15][r & 15];
+                    static_cast<float *>(a.work)[((int64_t)piece * a.tokens + t0 + t) * a.rank + r] = sum * gain;
+                }
+            }
+            __syncthreads();
         }
-        sum += add;
     }
-    a.out[t * a.ld_out + row] = sum;
 }
 
-int64_t adapters_work(const bq_adapters &a) { return a.tokens * a.rank * 4; }
+// out[t][row] = y[t][row] + B[row] . u[t]: 64 rows of B a wavefront, in
+// registers, along the result's rows; 16 NT tokens along its columns.  The
+// pieces of u are added up once for the workgroup's wavefronts, in LDS.
+template <class T, int KS, int NT>
+__global__ __launch_bounds__(256) void adapters_up(const AdapterArgs g)
+{
+    typedef T t8 __attribute__((ext_vector_type(8)));
+    __shared__ float us[16 * NT][32 * KS + 4];
+    const bq_adapters &a = g.a;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, q4 = lane >> 4;
+    const int64_t row0 = (int64_t)blockIdx.y * kUpRows + 64 * wave;
+    // four rows at a time where every row of y and out starts at a multiple of 16 bytes
+    const bool wide = (((uintptr_t)a.y | (uintptr_t)a.out | (uintptr_t)(4 * a.ld_y) | (uintptr_t)(4 * a.ld_out)) & 15) == 0;
+    int b, first, end;
+    for (int item = blockIdx.x; adapter_item<16 * NT>(g, item, b, first, end); item += gridDim.x) {
+        const int id = uniform_word(a.ids + b);
+        const bool has = (unsigned)id < (unsigned)a.count;
+        if (!has && a.y == a.out)
+            continue;
+        t8 w[4][KS];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t row = min(row0 + 16 * r + c16, a.rows - 1);
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+                w[r][k] = has && 32 * k + 8 * q4 < a.rank
+                              ? *reinterpret_cast<const t8 *>(static_cast<const T *>(a.b) + ((int64_t)id * a.rows + row) * a.rank + 32 * k + 8 * q4)
+                              : t8{};
+        }
+        for (int t0 = first; t0 < end; t0 += 16 * NT) {
+            f32x4 sum[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = t0 + 16 * n + c16;
+                    const int64_t row = row0 + 16 * r + 4 * q4;
+                    const float *y = a.y + (int64_t)t * a.ld_y + row;
+                    sum[n][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    if (wide && row + 4 <= a.rows) {
+                        if (t < end)
+                            sum[n][r] = *reinterpret_cast<const f32x4 *>(y);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (t < end && row + e < a.rows)
+                                sum[n][r][e] = y[e];
+                    }
+                }
+            if (has) {
+                // four ranks of a token at a time; the loads of four pieces, for all that a thread has, before their sums
+                constexpr int QUADS = 16 * NT * 8 * KS, MINE = (QUADS + 255) / 256;
+                f32x4 u[MINE];
+#pragma unroll
+                for (int i = 0; i < MINE; ++i)
+                    u[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int j = 0; j < g.pieces; j += 4) {
+                    f32x4 x[MINE][4];
+#pragma unroll
+                    for (int i = 0; i < MINE; ++i) {
+                        const int q = threadIdx.x + 256 * i, r = q % (8 * KS) * 4, t = t0 + q / (8 * KS);
+                        const float *p = static_cast<const float *>(a.work) + (int64_t)t * a.rank + r;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            x[i][k] = q < QUADS && r < a.rank && t < end && j + k < g.pieces
+                                          ? *reinterpret_cast<const f32x4 *>(p + (int64_t)(j + k) * a.tokens * a.rank)
+                                          : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    }
+#pragma unroll
+                    for (int i = 0; i < MINE; ++i)
+                        u[i] += (x[i][0] + x[i][1]) + (x[i][2] + x[i][3]);
+                }
+#pragma unroll
+                for (int i = 0; i < MINE; ++i) {
+                    const int q = threadIdx.x + 256 * i;
+                    if (q < QUADS)
+                        *reinterpret_cast<f32x4 *>(&us[q / (8 * KS)][q % (8 * KS) * 4]) = u[i];
+                }
+                __syncthreads();
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    f32x4 acc[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        Step<T, float> s;
+                        s.set(*reinterpret_cast<const typename Step<T, float>::raw *>(&us[16 * n + c16][32 * k + 8 * q4]));
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            acc[r] = s.add(w[r][k], acc[r]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        sum[n][r] += acc[r];
+                }
+                __syncthreads();
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = t0 + 16 * n + c16;
+                    const int64_t row = row0 + 16 * r + 4 * q4;
+                    float *out = a.out + (int64_t)t * a.ld_out + row;
+                    if (wide && row + 4 <= a.rows) {
+                        if (t < end)
+                            *reinterpret_cast<f32x4 *>(out) = sum[n][r];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (t < end && row + e < a.rows)
+                                out[e] = sum[n][r][e];
+                    }
+                }
+        }
+    }
+}
+
+static AdapterArgs adapters_plan(const bq_adapters &a)
+{
+    AdapterArgs g;
+    g.a = a;
+    const int64_t most = a.max_new < a.tokens ? a.max_new : a.tokens;
+    g.direct = most <= 16;
+    // items: no request has more tiles than its tokens fill, all together no more than all tokens do
+    auto items = [&](int tokens) {
+        const int64_t all = a.tokens / tokens + a.requests, each = (most + tokens - 1) / tokens * a.requests;
+        return g.direct ? (int64_t)a.requests : all < each ? all : each;
+    };
+    const int64_t down = items(g.direct ? 16 : 32), up = items(g.direct ? 16 : 64);
+    // pieces of n until about two workgroups a compute unit run, none of fewer than 512 values
+    int64_t pieces = 512 / down, cap = a.n / 512;
+    pieces = pieces > cap ? cap : pieces;
+    pieces = pieces > kMaxPieces ? kMaxPieces : pieces < 1 ? 1 : pieces;
+    const int64_t steps = (a.n + kDownStep - 1) / kDownStep, per = (steps + pieces - 1) / pieces;
+    g.piece = (int)(per * kDownStep);
+    g.pieces = (int)((steps + per - 1) / per);
+    g.down_items = (int)(down < (1 << 24) ? down : 1 << 24);  // the kernels walk on from there
+    g.up_items = (int)(up < (1 << 24) ? up : 1 << 24);
+    return g;
+}
+
+int64_t adapters_work(const bq_adapters &a) { return adapters_plan(a).pieces * a.tokens * a.rank * 4; }
+
+template <class T, class X, int RT>
+static void down_nt(const AdapterArgs &g, hipStream_t st)
+{
+    const dim3 grid((unsigned)(g.down_items * g.pieces));
+    if (g.direct)
+        hipLaunchKernelGGL((adapters_down<T, X, RT, 1>), grid, dim3(256), 0, st, g);
+    else
+        hipLaunchKernelGGL((adapters_down<T, X, RT, 2>), grid, dim3(256), 0, st, g);
+}
+
+template <class T, class X>
+static void down_rank(const AdapterArgs &g, hipStream_t st)
+{
+    const int rank = g.a.rank;
+    rank <= 16 ? down_nt<T, X, 1>(g, st) : rank <= 32 ? down_nt<T, X, 2>(g, st)
+        : rank <= 64 ? down_nt<T, X, 4>(g, st) : down_nt<T, X, 8>(g, st);
+}
+
+template <class T, int KS>
+static void up_nt(const AdapterArgs &g, hipStream_t st)
+{
+    const dim3 grid((unsigned)g.up_items, (unsigned)((g.a.rows + kUpRows - 1) / kUpRows));
+    if (g.direct)
+        hipLaunchKernelGGL((adapters_up<T, KS, 1>), grid, dim3(256), 0, st, g);
+    else
+        hipLaunchKernelGGL((adapters_up<T, KS, 4>), grid, dim3(256), 0, st, g);
+}
+
+template <class T>
+static void adapters_type(const AdapterArgs &g, hipStream_t st)
+{
+    g.a.x_type == BQ_F32 ? down_rank<T, float>(g, st) : down_rank<T, T>(g, st);
+    g.a.rank <= 32 ? up_nt<T, 1>(g, st) : g.a.rank <= 64 ? up_nt<T, 2>(g, st) : up_nt<T, 4>(g, st);
+}
 
 hipError_t launch_adapters(const bq_adapters &a, hipStream_t st)
 {
-    const dim3 down((unsigned)a.tokens), up((unsigned)a.tokens, (unsigned)((a.rows + 255) / 256));
-    if (a.type == BQ_F16) {
-        if (a.x_type == BQ_F32)
-            hipLaunchKernelGGL((adapters_down<_Float16, float>), down, dim3(256), 0, st, a);
-        else
-            hipLaunchKernelGGL((adapters_down<_Float16, _Float16>), down, dim3(256), 0, st, a);
-        hipLaunchKernelGGL((adapters_up<_Float16>), up, dim3(256), 0, st, a);
-    } else {
-        if (a.x_type == BQ_F32)
-            hipLaunchKernelGGL((adapters_down<__bf16, float>), down, dim3(256), 0, st, a);
-        else
-            hipLaunchKernelGGL((adapters_down<__bf16, __bf16>), down, dim3(256), 0, st, a);
-        hipLaunchKernelGGL((adapters_up<__bf16>), up, dim3(256), 0, st, a);
-    }
+    const AdapterArgs g = adapters_plan(a);
+    a.type == BQ_F16 ? adapters_type<_Float16>(g, st) : adapters_type<__bf16>(g, st);
     return hipGetLastError();
 }
 
