@@ -344,9 +344,9 @@ static AdapterArgs adapters_plan(const bq_adapters &a)
         const int64_t all = a.tokens / tokens + a.requests, each = (most + tokens - 1) / tokens * a.requests;
         return g.direct ? (int64_t)a.requests : all < each ? all : each;
     };
-    const int64_t down = items(g.direct ? 16 : 32), up = items(g.direct ? 16 : 64);
-    // pieces of n until about two workgroups a compute unit run, none of fewer than 512 values
-    int64_t pieces = 512 / down, cap = a.n / 512;
+    const int64_t down = items(g.direct ? 16 : 32), up = items(g.direct ? 16 : 32);
+    // pieces of n until a workgroup a compute unit runs, none of fewer than 512 values
+    int64_t pieces = 256 / down, cap = a.n / 512;
     pieces = pieces > cap ? cap : pieces;
     pieces = pieces > kMaxPieces ? kMaxPieces : pieces < 1 ? 1 : pieces;
     const int64_t steps = (a.n + kDownStep - 1) / kDownStep, per = (steps + pieces - 1) / pieces;
@@ -384,7 +384,7 @@ static void up_nt(const AdapterArgs &g, hipStream_t st)
     if (g.direct)
         hipLaunchKernelGGL((adapters_up<T, KS, 1>), grid, dim3(256), 0, st, g);
     else
-        hipLaunchKernelGGL((adapters_up<T, KS, 4>), grid, dim3(256), 0, st, g);
+        hipLaunchKernelGGL((adapters_up<T, KS, 2>), grid, dim3(256), 0, st, g);
 }
 
 template <class T>

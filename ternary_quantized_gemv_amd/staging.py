@@ -12,8 +12,9 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (Act, GroupCall, Weights, bq_quantize_act_q8, bq_quantize_act_q8_f16, bq_sweep_create,
-               bq_sweep_create_x, bq_token_sweep, BLOCK_LEN)
+from . import (Act, BQ_Q1_0, GroupCall, Weights, bq_adapters_add, bq_kv_append, bq_paged_attn, bq_q1_0_matvec, bq_q2_0_matvec,
+               bq_quantize_act_q8, bq_quantize_act_q8_f16, bq_rmsnorm_q8, bq_sweep_create, bq_sweep_create_x, bq_token_sweep,
+               BLOCK_LEN)
 
 
 class StagedSweep:
@@ -199,3 +200,78 @@ class StagedChain:
             for _, _, _, plan in self.stages:
                 plan.destroy()
         self.stages = []
+
+
+# --------------------------------------------------------------- attention
+class StagedAttention:
+    """The attention block of a decoder layer between its packed products, for
+    the new tokens of any number of requests: residual addition, norm and
+    8-bit activation; q, k and v products; their adapters; norm, rotation and
+    cache; attention over the cache; quantizer; o product.  One token per
+    request is a decode step, whole prompts and chunks of them run the same
+    way (the products take up to 16 tokens, the columns of a call, at a time).
+
+    All buffers hold max_tokens rows and are allocated here, so that run()
+    allocates nothing and can be captured into a graph; run() of two blocks on
+    two streams need two objects."""
+
+    COLUMNS = 16  # activation columns of one product call
+
+    def __init__(self, fmt: int, canon, hidden: int, q_heads: int, cache, norm, freq, max_tokens: int, qa: int = 128,
+                 q_norm=None, k_norm=None, adapters=None, eps: float = 1e-6):
+        """canon: {"q", "k", "v", "o"} canonical matrices ([q_heads * dim or
+        heads * dim, hidden] and [hidden, q_heads * dim]); cache: KVCache;
+        norm: float32 [hidden]; adapters: {"q" / "k" / "v" / "o": Adapters}."""
+        import torch
+
+        self.fmt, self.hidden, self.q_heads, self.cache, self.qa, self.eps = fmt, hidden, q_heads, cache, qa, eps
+        nq, nk = q_heads * cache.dim, cache.heads * cache.dim
+        self.weights = {}
+        for name, rows, cols in (("q", nq, hidden), ("k", nk, hidden), ("v", nk, hidden), ("o", hidden, nq)):
+            if cols % qa or cols % BLOCK_LEN[fmt]:
+                raise ValueError("every cols must be a multiple of qa and of the block length")
+            self.weights[name] = Weights.upload(fmt, canon[name], rows, cols)
+        self.norm, self.freq, self.q_norm, self.k_norm = norm, freq, q_norm, k_norm
+        self.adapters = adapters or {}
+
+        def rows(n, dtype=torch.float32):
+            return torch.empty(max_tokens, n, dtype=dtype, device="cuda")
+
+        self.h, self.normed = rows(hidden), rows(hidden)
+        self.act, self.act_d = rows(hidden, torch.int8), rows(hidden // qa)
+        self.q, self.k, self.v, self.o = rows(nq), rows(nk), rows(nk), rows(nq)
+        self.o_act, self.o_d, self.out = rows(nq, torch.int8), rows(nq // qa), rows(hidden)
+
+    def _product(self, name: str, act, d, y, tokens: int, stream):
+        w = self.weights[name]
+        call = bq_q1_0_matvec if self.fmt == BQ_Q1_0 else bq_q2_0_matvec
+        for c in range(0, tokens, self.COLUMNS):
+            e = min(tokens, c + self.COLUMNS)
+            call(w, Act(act[c:e], d[c:e], w.cols, self.qa, e - c), y[c:e], stream)
+
+    def run(self, x, res, pos, slot, cu, lens, table, max_new: int, max_keys: int, ids=None, work=None,
+            adapter_work=None, stream=None):
+        """x, res: float32 [tokens, hidden] (res: the residual stream, None for
+        the first block); the rest as in bq_kv_append, bq_paged_attn and
+        bq_adapters_add.  Returns (out, h): this block's output and the
+        residual stream that it is to be added to.  With work and adapter_work
+        given, nothing is allocated."""
+        T = x.shape[0]
+        cache, dim = self.cache, self.cache.dim
+        q, k, v, o, h, out = (b[:T] for b in (self.q, self.k, self.v, self.o, self.h, self.out))
+        normed = self.normed[:T] if self.adapters else None
+        bq_rmsnorm_q8(x, self.norm, self.eps, self.qa, self.act[:T], self.act_d[:T], res=res, h=h, y=normed, stream=stream)
+        for name, y in (("q", q), ("k", k), ("v", v)):
+            self._product(name, self.act, self.act_d, y, T, stream)
+            if name in self.adapters:
+                bq_adapters_add(self.adapters[name], normed, cu, ids, max_new, y, work=adapter_work, stream=stream)
+        heads = (T, self.q_heads, dim)
+        bq_kv_append(cache, k.view(T, cache.heads, dim), v.view(T, cache.heads, dim), pos, slot, self.freq, q=q.view(heads),
+                     q_out=q.view(heads), q_norm=self.q_norm, k_norm=self.k_norm, eps=self.eps, stream=stream)
+        bq_paged_attn(cache, q.view(heads), cu, lens, table, dim ** -0.5, max_new, max_keys, o.view(heads), work=work,
+                      stream=stream)
+        bq_quantize_act_q8(o.view(-1), self.qa, self.o_act[:T].view(-1), self.o_d[:T].view(-1), stream)
+        self._product("o", self.o_act, self.o_d, out, T, stream)
+        if "o" in self.adapters:
+            bq_adapters_add(self.adapters["o"], o, cu, ids, max_new, out, work=adapter_work, stream=stream)
+        return out, h
