@@ -42,7 +42,7 @@ struct AppendArgs {
     bq_append a;
     int qk_blocks;   // workgroups of the query and key heads, then those of the values
     int splits;      // workgroups per token of the former
-    int v_cols;      // workgroups per eight tokens of the latter
+    int v_cols;      // workgroups per 64 tokens of the latter
 };
 
 // 8 values a lane, D / 8 neighbouring lanes a head.  T: type of the rows, C: of the cache.
@@ -112,52 +112,59 @@ __device__ __forceinline__ void append_qk(const AppendArgs &g, float *cs)
     }
 }
 
-// Eight tokens, 256 value columns: a thread owns one column (head, index).
-// Eight tokens whose places are neighbours in a page, from a multiple of
-// eight on, are one 16-byte store; the workgroup with the first of them makes
-// it and those of the others leave them out.
+// About 64 tokens, 64 value columns: a lane owns a column (head, index), a
+// wavefront eight tokens at a time.  Eight tokens whose places are neighbours
+// in a page, from a multiple of eight on, are one 16-byte store a lane; so the
+// tile starts up to seven tokens early, where its first token's run has such a
+// place, and takes up to seven more tokens than the 64 that its neighbours
+// leave (what two tiles both take they write alike).  64 tokens because a
+// page's row of them is a whole cache line then: one L2 has all its parts.
+constexpr int kValueTokens = 64, kValueCols = 64;
+
 template <class T, class C, int D>
-__device__ __forceinline__ void append_v(const AppendArgs &g, int64_t block, int *how)
+__device__ __forceinline__ void append_v(const AppendArgs &g, int64_t block)
 {
     const bq_append &a = g.a;
-    const int64_t t0 = block / g.v_cols * 8;
-    const int col = (int)(block % g.v_cols) * kAppendThreads + threadIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t tile = block / g.v_cols * kValueTokens;
+    const int col = (int)(block % g.v_cols) * kValueCols + lane;
     const int64_t places = a.cache.pages * a.cache.page;
-    if (threadIdx.x < 8) {
-        const int64_t t = t0 + threadIdx.x;
-        int f = 0;  // nothing to store
-        if (t < a.tokens) {
-            const int64_t slot = a.slot[t];
-            if (slot >= 0 && slot < places) {
-                const int64_t first = t - (slot & 7);
-                bool run = first >= 0 && first + 8 <= a.tokens;
-                for (int i = 0; i < 8 && run; ++i)
-                    run = a.slot[first + i] == (slot & ~(int64_t)7) + i;
-                f = !run ? 1 : (slot & 7) == 0 ? 2 : 0;
-            }
-        }
-        how[threadIdx.x] = f;
-    }
-    __syncthreads();
-    if (col >= a.cache.heads * D)
-        return;
+    const int64_t start = a.slot[tile];
+    const int64_t from = tile - (start > 0 ? start & 7 : 0);
     const int h = col / D, d = col % D;
     const T *src = static_cast<const T *>(a.v) + col;
-    for (int i = 0; i < 8; ++i) {
-        const int f = how[i];
-        if (!f)
-            continue;
-        const int64_t t = t0 + i, slot = a.slot[t];
-        const int64_t page = slot / a.cache.page, off = slot % a.cache.page;
-        C *dst = static_cast<C *>(a.cache.v) + ((page * a.cache.heads + h) * D + d) * a.cache.page + off;
-        if (f == 1) {
-            *dst = (C)(float)src[t * a.ld_v];
-        } else {
-            float v[8];
+    C *dst = static_cast<C *>(a.cache.v) + (int64_t)(h * D + d) * a.cache.page;
+    const int64_t page_elems = (int64_t)a.cache.heads * D * a.cache.page;
+    const int log2 = __builtin_ctz((unsigned)a.cache.page);
+    for (int i = wave; i < kValueTokens / 8 + 1; i += kAppendThreads / 64) {
+        const int64_t t0 = from + 8 * i;
+        if (t0 >= a.tokens)
+            break;
+        T v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t t = t0 + e < 0 ? 0 : t0 + e < a.tokens ? t0 + e : a.tokens - 1;
+            v[e] = src[t * a.ld_v];
+        }
+        // lanes 0 .. 7 (and every eighth of them again): the place of token t0 + lane % 8
+        const int64_t t = t0 + (lane & 7);
+        int64_t slot = t >= 0 && t < a.tokens ? a.slot[t] : -1;
+        slot = slot < places ? slot : -1;
+        const int64_t first = __shfl(slot, 0, 64);
+        if (__all(first >= 0 && (first & 7) == 0 && slot == first + (lane & 7))) {
+            C *p = dst + (first >> log2) * page_elems + (first & (a.cache.page - 1));
+            float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[e] = (float)src[(t + e) * a.ld_v];
-            store8(dst, v);
+                x[e] = (float)v[e];
+            store8(p, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t to = __shfl(slot, e, 64);
+                if (to >= 0)
+                    dst[(to >> log2) * page_elems + (to & (a.cache.page - 1))] = (C)(float)v[e];
+            }
         }
     }
 }
@@ -166,11 +173,10 @@ template <class T, class C, int D>
 __global__ __launch_bounds__(kAppendThreads) void append_kernel(const AppendArgs g)
 {
     __shared__ float cs[128];
-    __shared__ int how[8];
     if ((int)blockIdx.x < g.qk_blocks)
         append_qk<T, C, D>(g, cs);
     else
-        append_v<T, C, D>(g, (int64_t)blockIdx.x - g.qk_blocks, how);
+        append_v<T, C, D>(g, (int64_t)blockIdx.x - g.qk_blocks);
 }
 
 template <class T, class C>
@@ -191,8 +197,8 @@ hipError_t launch_append(const bq_append &a, hipStream_t st)
     // few tokens: a workgroup per round of heads; many: all heads share one workgroup's angles
     g.splits = a.tokens < 512 ? rounds : 1;
     g.qk_blocks = (int)(a.tokens * g.splits);
-    g.v_cols = (a.cache.heads * a.cache.dim + kAppendThreads - 1) / kAppendThreads;
-    const unsigned blocks = (unsigned)(g.qk_blocks + (a.tokens + 7) / 8 * g.v_cols);
+    g.v_cols = a.cache.heads * a.cache.dim / kValueCols;
+    const unsigned blocks = (unsigned)(g.qk_blocks + (a.tokens + kValueTokens - 1) / kValueTokens * g.v_cols);
     if (a.type == BQ_F32)
         a.cache.type == BQ_F16 ? append_dim<float, _Float16>(g, blocks, st) : append_dim<float, __bf16>(g, blocks, st);
     else if (a.type == BQ_F16)
