@@ -116,10 +116,10 @@ def _rows(fn: str, what: str, t, dtype, dev: int, shape):
     """(pointer, elements between rows) of a tensor of this shape whose rows
     (all dimensions but the first) are contiguous; a single row may come
     without its first dimension."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr(), t.stride(0)
     _tensor(fn, what, t, dtype, dev)
     have, stride = t.shape, t.stride()
-    if have == shape and t.is_contiguous():
-        return t.data_ptr(), stride[0]
     if len(have) == len(shape) - 1 and shape[0] == 1:
         have, stride = (1, *have), (0, *stride)
     if tuple(have) != shape:
@@ -134,10 +134,18 @@ def _rows(fn: str, what: str, t, dtype, dev: int, shape):
 
 def _flat(fn: str, what: str, t, dtype, dev: int, n: int) -> int:
     """Pointer of a contiguous tensor of n values."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     _tensor(fn, what, t, dtype, dev)
-    if t.numel() != n or not t.is_contiguous():
-        _refuse(fn, f"{what} must be contiguous with {n} values, has shape {tuple(t.shape)}")
-    return t.data_ptr()
+    _refuse(fn, f"{what} must be contiguous with {n} values, has shape {tuple(t.shape)}")
+
+
+def _whole(fn: str, what: str, t, dtype, dev: int, shape) -> int:
+    """Pointer of a contiguous tensor of this shape."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _tensor(fn, what, t, dtype, dev)
+    _refuse(fn, f"{what} must be contiguous with shape {tuple(shape)}, has {tuple(t.shape)}")
 
 
 # the stream and device lookups without the objects that torch.cuda makes of them
@@ -206,12 +214,10 @@ class KVCache:
         if k.dim() != 4:
             _refuse(fn, "k must be [pages, heads, page, dim]")
         self.pages, self.heads, self.page, self.dim = pages, heads, page, dim = k.shape
-        kp = _rows(fn, "k", k, k.dtype, dev, (pages, heads, page, dim))[0]
-        vp = _rows(fn, "v", v, k.dtype, dev, (pages, heads, dim, page))[0]
-        if not k.is_contiguous() or not v.is_contiguous():
-            _refuse(fn, "k and v must be contiguous")
+        dt = k.dtype
         self.k, self.v = k, v
-        self.c = (_type(fn, "k", k), heads, dim, page, pages, kp, vp)
+        self.c = (_type(fn, "k", k), heads, dim, page, pages, _whole(fn, "k", k, dt, dev, k.shape),
+                  _whole(fn, "v", v, dt, dev, (pages, heads, dim, page)))
 
     @classmethod
     def empty(cls, pages: int, heads: int, dim: int, page: int = 64, dtype=torch.bfloat16, device="cuda"):
@@ -312,11 +318,9 @@ class Adapters:
             _refuse(fn, "a must be [count, rank, n] and b [count, rows, rank]")
         self.count, self.rank, self.n = count, rank, n = a.shape
         self.rows = rows = b.shape[1]
-        ap = _rows(fn, "a", a, a.dtype, dev, (count, rank, n))[0]
-        bp = _rows(fn, "b", b, a.dtype, dev, (count, rows, rank))[0]
-        if not a.is_contiguous() or not b.is_contiguous():
-            _refuse(fn, "a and b must be contiguous")
-        self.pointers = (ap, bp, _flat(fn, "gain", gain, torch.float32, dev, count))
+        dt = a.dtype
+        self.pointers = (_whole(fn, "a", a, dt, dev, a.shape), _whole(fn, "b", b, dt, dev, (count, rows, rank)),
+                         _flat(fn, "gain", gain, torch.float32, dev, count))
         self.a, self.b, self.gain = a, b, gain
         self.type = _type(fn, "a", a)
 
