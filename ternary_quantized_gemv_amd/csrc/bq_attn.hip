@@ -27,7 +27,6 @@
 
 namespace bq {
 
-constexpr int kAttnWaves = 4;
 constexpr int kAttnKeys = 32;   // keys of a wavefront at a time
 constexpr int kAttnStep = 128;  // keys that a workgroup's wavefronts take at most at a time
 constexpr int kMaxChunks = 128; // pieces of a row's keys that the joins take
@@ -143,16 +142,16 @@ __device__ __forceinline__ bool few_item(const AttnArgs &g, int item, int chunk_
     return false;
 }
 
-// CW of the four wavefronts take 16 NT columns each, the others the same
-// columns over other keys.
-template <int CT, int D, int NT, int CW, bool F32>
-__global__ __launch_bounds__(64 * kAttnWaves, NT == 1 && !F32 ? 3 : 2) void attn_kernel(const AttnArgs g)
+// CW of the W wavefronts take 16 NT columns each, the others the same columns
+// over other keys.
+template <int CT, int D, int NT, int CW, int W, bool F32>
+__global__ __launch_bounds__(64 * W, NT == 1 && !F32 ? 3 : 2) void attn_kernel(const AttnArgs g)
 {
     typedef typename Num<CT>::t T;
     typedef typename Num<CT>::v8 v8;
     constexpr int NP = F32 ? Parts<T>::n : 1;
     constexpr int DJ = D / 32, DT = D / 16;
-    constexpr int KW = kAttnWaves / CW, COLS = 16 * NT * CW;  // wavefronts along the keys, rows of a tile
+    constexpr int KW = W / CW, COLS = 16 * NT * CW;  // wavefronts along the keys, rows of a tile
     __shared__ float sm[KW][COLS], sl[KW][COLS];
     __shared__ float so[KW][COLS][D + 4];
 
@@ -323,7 +322,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, NT == 1 && !F32 ? 3 : 2) void attn
         }
         __syncthreads();
         // ---- out, or this chunk's part of it
-        for (int u = threadIdx.x; u < COLS * (D / 8); u += 64 * kAttnWaves) {
+        for (int u = threadIdx.x; u < COLS * (D / 8); u += 64 * W) {
             const int cr = u / (D / 8), d8 = u % (D / 8) * 8, r = r0 + cr;
             if (r >= rows)
                 continue;
@@ -501,8 +500,9 @@ AttnPlan attn_plan(const bq_attn &a)
         p.few.cols = rows <= 16 || rows > kFewRows ? 16 : rows <= 32 ? 32 : 64;
         const int64_t tiles = ((rows > kFewRows ? kFewRows : rows) + p.few.cols - 1) / p.few.cols;
         const int64_t units = (a.max_keys + kAttnStep - 1) / kAttnStep;
-        // as many pieces as workgroups fit the 256 compute units at once: three where 170 registers allow it
-        const int64_t want = p.few.cols == 16 && a.type != BQ_F32 ? 768 : 512;
+        // as many pieces as workgroups fit the 256 compute units at once: one of eight wavefronts, two of four,
+        // three of four where 170 registers are enough
+        const int64_t want = p.few.cols == 64 ? 256 : p.few.cols == 16 && a.type != BQ_F32 ? 768 : 512;
         const int64_t items = want / heads < 1 ? 1 : want / heads;
         const int64_t cut = units < 1 ? 1 : units, each = tiles * a.requests;
         // no row has more pieces than units, nor than the items if they are all its own
@@ -538,9 +538,9 @@ template <int CT, int D, bool F32>
 static void attn_nt(const AttnArgs &g, dim3 grid, hipStream_t st)
 {
     switch (g.p.few.cols) {
-    case 16: hipLaunchKernelGGL((attn_kernel<CT, D, 1, 1, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
-    case 32: hipLaunchKernelGGL((attn_kernel<CT, D, 1, 2, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
-    default: hipLaunchKernelGGL((attn_kernel<CT, D, 2, 2, F32>), grid, dim3(64 * kAttnWaves), 0, st, g); break;
+    case 16: hipLaunchKernelGGL((attn_kernel<CT, D, 1, 1, 4, F32>), grid, dim3(256), 0, st, g); break;
+    case 32: hipLaunchKernelGGL((attn_kernel<CT, D, 1, 2, 4, F32>), grid, dim3(256), 0, st, g); break;
+    default: hipLaunchKernelGGL((attn_kernel<CT, D, 2, 2, 8, F32>), grid, dim3(512), 0, st, g); break;
     }
 }
 
