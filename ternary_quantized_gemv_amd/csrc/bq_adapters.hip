@@ -29,55 +29,33 @@ struct AdapterArgs {
     int direct;       // item i is request i (few tokens each), else the items of all requests are counted through
 };
 
-// Item `item` of 16 NT tokens each: request b, its rows and where they start.
+// Item `item` of TOKENS tokens each: request b, its rows and where they start.
 // With `direct` a request is one item, which walks its rows.
 template <int TOKENS>
-__device__ __forceinline__ bool adapter_item(const AdapterArgs &g, int item, int &b, int &first, int &end)
+__device__ __forceinline__ bool adapter_item(const AdapterArgs &g, Walk &w, int item, int &b, int &first, int &end)
 {
     const bq_adapters &a = g.a;
-    auto rows_of = [&](int i, int &lo) {
-        lo = a.cu[i];
-        int hi = a.cu[i + 1];
-        hi = hi > a.tokens ? (int)a.tokens : hi;
-        return lo < 0 || hi < lo ? 0 : hi - lo;
-    };
+    int within = 0;
     if (g.direct) {
         if (item >= a.requests)
             return false;
         b = item;
-        first = uniform_word(a.cu + b);
-        end = uniform_word(a.cu + b + 1);
-        end = end > a.tokens ? (int)a.tokens : end;
-        if (first < 0)
-            end = first = 0;
-        return true;
+    } else if (!find_item(w, a.requests, item, b, within, [&](int i) {
+                   const int lo = a.cu[i], hi = a.cu[i + 1] > a.tokens ? (int)a.tokens : a.cu[i + 1];
+                   return lo < 0 || hi < lo ? 0 : (hi - lo + TOKENS - 1) / TOKENS;
+               })) {
+        return false;
     }
-    const int lane = threadIdx.x & 63;
-    int before = 0;
-    for (int base = 0; base < a.requests; base += 64) {
-        int lo = 0, n = 0;
-        if (base + lane < a.requests)
-            n = rows_of(base + lane, lo);
-        const int mine = (n + TOKENS - 1) / TOKENS;
-        int upto = mine;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int x = __shfl_up(upto, off, 64);
-            upto += lane >= off ? x : 0;
-        }
-        const unsigned long long has = __ballot(item - before < upto);
-        if (has) {
-            const int at = __builtin_ctzll(has);
-            b = base + at;
-            const int within = item - before - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at));
-            const int l = __builtin_amdgcn_readlane(lo, at), m = __builtin_amdgcn_readlane(n, at);
-            first = l + within * TOKENS;
-            end = min(first + TOKENS, l + m);
-            return true;
-        }
-        before += __builtin_amdgcn_readlane(upto, 63);
+    first = uniform_word(a.cu + b);
+    end = uniform_word(a.cu + b + 1);
+    end = end > a.tokens ? (int)a.tokens : end;
+    if (first < 0)
+        end = first = 0;
+    if (!g.direct) {
+        first += within * TOKENS;
+        end = min(end, first + TOKENS);
     }
-    return false;
+    return true;
 }
 
 // c += W X^T for 32 values of k: weights w (16 bits), values x as f32 or of the weights' type.
@@ -144,8 +122,9 @@ __global__ __launch_bounds__(256) void adapters_down(const AdapterArgs g)
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, q4 = lane >> 4;
     const int piece = blockIdx.x % g.pieces;
     const int64_t from = (int64_t)piece * g.piece, to = min(from + g.piece, a.n);
+    Walk walk;
     int b, first, end;
-    for (int item = blockIdx.x / g.pieces; adapter_item<16 * NT>(g, item, b, first, end); item += gridDim.x / g.pieces) {
+    for (int item = blockIdx.x / g.pieces; adapter_item<16 * NT>(g, walk, item, b, first, end); item += gridDim.x / g.pieces) {
         const int id = uniform_word(a.ids + b);
         if ((unsigned)id >= (unsigned)a.count)
             continue;
@@ -226,8 +205,9 @@ __global__ __launch_bounds__(256) void adapters_up(const AdapterArgs g)
     const int64_t row0 = (int64_t)blockIdx.y * kUpRows + 64 * wave;
     // four rows at a time where every row of y and out starts at a multiple of 16 bytes
     const bool wide = (((uintptr_t)a.y | (uintptr_t)a.out | (uintptr_t)(4 * a.ld_y) | (uintptr_t)(4 * a.ld_out)) & 15) == 0;
+    Walk walk;
     int b, first, end;
-    for (int item = blockIdx.x; adapter_item<16 * NT>(g, item, b, first, end); item += gridDim.x) {
+    for (int item = blockIdx.x; adapter_item<16 * NT>(g, walk, item, b, first, end); item += gridDim.x) {
         const int id = uniform_word(a.ids + b);
         const bool has = (unsigned)id < (unsigned)a.count;
         if (!has && a.y == a.out)

@@ -49,6 +49,17 @@ __device__ __forceinline__ Request request_at(const bq_attn &a, int b)
     return r;
 }
 
+// The same for a request of each lane: rows of query heads (0: not this
+// kernel's, which `few` says) and keys.
+__device__ __forceinline__ void lane_request(const AttnArgs &g, int b, bool few, int &rows, int &keys)
+{
+    const int lo = g.a.cu[b], hi = g.a.cu[b + 1], len = g.a.lens[b];
+    const int n = lo < 0 ? 0 : (hi > g.a.tokens ? (int)g.a.tokens : hi) - lo;
+    const int64_t most = (int64_t)g.a.table_cols * g.a.cache.page;
+    rows = n > 0 && has_few(g.p, n * g.group) == few ? n * g.group : 0;
+    keys = len < 0 ? 0 : len > most ? (int)most : len;
+}
+
 // Page of the 16 keys from `key` (a multiple of 16, the same in all lanes) of a
 // request, -1 where there is none.
 __device__ __forceinline__ int page_at(const AttnArgs &g, const int32_t *table, int key, int end)
@@ -166,6 +177,12 @@ __device__ __forceinline__ float2 *part_stats(const AttnArgs &g, int64_t row, in
 {
     float *end = static_cast<float *>(g.a.work) + g.a.tokens * g.a.q_heads * g.p.stride * dim;
     return reinterpret_cast<float2 *>(end) + row * g.p.stride + c;
+}
+// Behind those, the units of a piece of few rows' keys: the kernel leaves its
+// cut to the join.
+__device__ __forceinline__ int32_t *part_units(const AttnArgs &g, int dim)
+{
+    return reinterpret_cast<int32_t *>(part_stats(g, g.a.tokens * g.a.q_heads, 0, dim));
 }
 
 hipError_t launch_attn_tiles(const AttnArgs &g, hipStream_t st);

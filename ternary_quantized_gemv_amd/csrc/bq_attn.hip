@@ -40,21 +40,9 @@ constexpr int kMaxChunks = 128; // pieces of a row's keys that the joins take
 // `chunk` of them a piece, so that the pieces are about few.items per key head
 // and at most g.p.stride per row.
 
-// Lane i: tiles of rows and units of keys of request `i` (0 if it is not this kernel's).
-__device__ __forceinline__ void few_request(const AttnArgs &g, int i, int &tiles, int &units)
-{
-    tiles = units = 0;
-    if (i >= g.a.requests)
-        return;
-    const int lo = g.a.cu[i], hi = g.a.cu[i + 1], len = g.a.lens[i];
-    const int n = lo < 0 ? 0 : (hi > g.a.tokens ? (int)g.a.tokens : hi) - lo;
-    const int64_t most = (int64_t)g.a.table_cols * g.a.cache.page, rows = (int64_t)n * g.group;
-    if (n <= 0 || !has_few(g.p, (int)rows))
-        return;
-    tiles = ((int)rows + g.p.few.cols - 1) / g.p.few.cols;
-    units = ((len > most ? (int)most : len) + kAttnStep - 1) / kAttnStep;
-    units = units < 1 ? 1 : units;  // no keys: one piece, of zeros
-}
+// Tiles of rows and units of keys; a request without keys has one piece, of zeros.
+__device__ __forceinline__ int few_tiles(const AttnArgs &g, int rows) { return (rows + g.p.few.cols - 1) / g.p.few.cols; }
+__device__ __forceinline__ int few_units(int keys) { return keys > kAttnStep ? (keys + kAttnStep - 1) / kAttnStep : 1; }
 
 __device__ __forceinline__ float wave_sum(float x)
 {
@@ -66,19 +54,24 @@ __device__ __forceinline__ float wave_sum(float x)
 
 // Units of a piece: those of all requests over the pieces wanted, and, as every
 // request rounds its pieces up, more where that made too many (twice: pieces
-// that fill the GPU once and a third take as long as two fillings).  Sums in
-// f32: the same in every workgroup, and exact enough.
-__device__ __forceinline__ int few_chunk(const AttnArgs &g, int tiles0, int units0)
+// that fill the GPU once and a third take as long as two fillings; not for so
+// many requests that they even out).  Sums in f32: the same in every
+// workgroup, and exact enough.
+__device__ __forceinline__ int few_chunk(const AttnArgs &g)
 {
     const int lane = threadIdx.x & 63;
     const float want = (float)g.p.few.items;
-    float total = (float)tiles0 * (float)units0;
-    int most = units0;
-    for (int base = 64; base < g.a.requests; base += 64) {
-        int t, u;
-        few_request(g, base + lane, t, u);
-        total += (float)t * (float)u;
-        most = max(most, u);
+    float total = 0.0f;
+    int most = 1, tiles = 0, units = 1;
+#pragma unroll 4
+    for (int base = 0; base < g.a.requests; base += 64) {
+        int rows = 0, keys = 0;
+        if (base + lane < g.a.requests)
+            lane_request(g, base + lane, true, rows, keys);
+        tiles = few_tiles(g, rows);
+        units = few_units(keys);
+        total += (float)tiles * (float)units;
+        most = max(most, tiles ? units : 1);
     }
     if (g.a.requests > 1) {
         total = wave_sum(total);
@@ -88,58 +81,14 @@ __device__ __forceinline__ int few_chunk(const AttnArgs &g, int tiles0, int unit
     }
     const int least = max((most + g.p.stride - 1) / g.p.stride, 1);
     int chunk = max((int)fminf(__builtin_ceilf(total / want), 16777216.0f), least);
-    if (g.a.requests > 1) {
+    if (g.a.requests > 1 && g.a.requests <= 64) {
         for (int again = 0; again < 2; ++again) {
-            float count = (float)(tiles0 * ((units0 + chunk - 1) / chunk));
-            for (int base = 64; base < g.a.requests; base += 64) {
-                int t, u;
-                few_request(g, base + lane, t, u);
-                count += (float)(t * ((u + chunk - 1) / chunk));
-            }
-            count = wave_sum(count);
+            const float count = wave_sum((float)(tiles * ((units + chunk - 1) / chunk)));
             if (count > want)
                 chunk = min(max((int)fminf(__builtin_ceilf((float)chunk * (count / want)), 16777216.0f), chunk + 1), max(most, least));
         }
     }
     return __builtin_amdgcn_readfirstlane(chunk);
-}
-
-// Item `item` of the pieces of all requests: request b, its tile and chunk, how
-// many chunks it has and the keys of each (a request's pieces are as even as
-// its units allow).  False where there are fewer items.
-__device__ __forceinline__ bool few_item(const AttnArgs &g, int item, int chunk_units, int tiles0, int units0, int &b,
-                                         int &tile, int &chunk, int &chunks, int &keys)
-{
-    const int lane = threadIdx.x & 63;
-    int before = 0;  // items of the requests in front
-    for (int base = 0; base < g.a.requests; base += 64) {
-        int t = tiles0, u = units0;
-        if (base)
-            few_request(g, base + lane, t, u);
-        const int c = (u + chunk_units - 1) / chunk_units, mine = t * c;
-        int upto = mine;
-        if (g.a.requests > 1) {
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-                const int x = __shfl_up(upto, off, 64);
-                upto += lane >= off ? x : 0;
-            }
-        }
-        const unsigned long long has = __ballot(item - before < upto);
-        if (has) {
-            const int at = __builtin_ctzll(has);
-            b = base + at;
-            const int within = item - before - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at));
-            const int ts = __builtin_amdgcn_readlane(t, at);
-            chunks = __builtin_amdgcn_readlane(c, at);
-            keys = (__builtin_amdgcn_readlane(u, at) + chunks - 1) / chunks * kAttnStep;
-            tile = within % ts;
-            chunk = within / ts;
-            return true;
-        }
-        before += __builtin_amdgcn_readlane(upto, 63);
-    }
-    return false;
 }
 
 // CW of the W wavefronts take 16 NT columns each, the others the same columns
@@ -166,14 +115,22 @@ __global__ __launch_bounds__(64 * W, NT == 1 && !F32 ? 3 : 2) void attn_kernel(c
     const int kofs = 8 * (c16 >> 2), vofs = 8 * q4;
     const T *kbase = static_cast<const T *>(a.cache.k) + (int64_t)kh * P * D + 8 * q4 + (c16 & 3) * D;
     const T *vbase = static_cast<const T *>(a.cache.v) + (int64_t)(kh * D + c16) * P;
-    int tiles0, units0;
-    few_request(g, lane, tiles0, units0);
-    const int chunk_units = few_chunk(g, tiles0, units0);
-
-    int b, tile, chunk, chunks, keys;
-    for (int item = blockIdx.y; few_item(g, item, chunk_units, tiles0, units0, b, tile, chunk, chunks, keys); item += gridDim.y) {
+    const int chunk_units = few_chunk(g);
+    if (g.p.stride > 1 && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+        *part_units(g, D) = chunk_units;
+    auto pieces = [&](int i) {
+        int rows, keys;
+        lane_request(g, i, true, rows, keys);
+        return few_tiles(g, rows) * ((few_units(keys) + chunk_units - 1) / chunk_units);
+    };
+    Walk walk;
+    int b, within;
+    for (int item = blockIdx.y; find_item(walk, a.requests, item, b, within, pieces); item += gridDim.y) {
         const Request rq = request_at(a, b);
-        const int rows = rq.n * g.group, r0 = tile * COLS;
+        const int rows = rq.n * g.group, tiles = few_tiles(g, rows), units = few_units(rq.keys);
+        // a request's pieces are as even as its units allow
+        const int chunks = (units + chunk_units - 1) / chunk_units, keys = (units + chunks - 1) / chunks * kAttnStep;
+        const int chunk = within / tiles, r0 = (within - chunk * tiles) * COLS;
         const int32_t *table = a.table + (int64_t)b * a.ld_table;
         // ---- the keys: those that the tile's last row sees, this workgroup's chunk of them
         const int last_row = min(r0 + COLS, rows) - 1;
@@ -377,10 +334,8 @@ __global__ __launch_bounds__(256) void attn_join_few(const AttnArgs g)
     const int64_t rows64 = (int64_t)rq.n * g.group;
     if (rq.n <= 0 || !has_few(g.p, (int)rows64) || (int64_t)blockIdx.x >= (int64_t)rq.n * a.q_heads)
         return;
-    int tiles0, units0;
-    few_request(g, lane, tiles0, units0);
-    const int chunk_units = few_chunk(g, tiles0, units0);
-    const int chunks = ((rq.keys + kAttnStep - 1) / kAttnStep + chunk_units - 1) / chunk_units;
+    const int chunk_units = uniform_word(part_units(g, D));
+    const int chunks = (few_units(rq.keys) + chunk_units - 1) / chunk_units;
     if (chunks <= 1)
         return;
     const int grp = threadIdx.x / L, d8 = threadIdx.x % L * 8;
@@ -508,18 +463,23 @@ AttnPlan attn_plan(const bq_attn &a)
         // no row has more pieces than units, nor than the items if they are all its own
         stride = cut < items ? cut : items;
         stride = stride > kMaxChunks ? kMaxChunks : stride;
-        const int64_t grid = items + each;
+        // a workgroup for every piece there can be; of more than 64 requests two fillings of the GPU, which look
+        // the requests up once and walk their pieces
+        int64_t grid = items + each < each * cut ? items + each : each * cut;
+        if (a.requests > 64 && grid > 2 * items)
+            grid = 2 * items;
         p.few.items = (int)items;
-        p.few.grid = (int)(grid < each * cut ? grid : each * cut < 65535 ? each * cut : 65535);
-        p.few.grid = p.few.grid > 65535 ? 65535 : p.few.grid;
+        p.few.grid = (int)(grid > 65535 ? 65535 : grid);
     }
     if (rows > kFewRows) {
         p.many.cols = rows <= 128 || a.type == BQ_F32 ? 128 : 256;
-        const int64_t tiles = (rows + p.many.cols - 1) / p.many.cols;
+        // tiles that can have rows: no request has more than its rows fill, all together no more than all rows do
+        // and one for each request of many rows
+        const int64_t all_rows = a.tokens * group, others = all_rows / kFewRows + 1;
+        const int64_t all = all_rows / p.many.cols + (others < a.requests ? others : a.requests);
+        const int64_t each = (rows + p.many.cols - 1) / p.many.cols * a.requests, tiles = each < all ? each : all;
         p.many.tiles = (int)(tiles < 32768 ? tiles : 32768);  // a grid dimension; the kernel walks on from there
-        // tiles that can have rows: no request has more than that, all together no more than the rows allow
-        const int64_t all = a.tokens * group / p.many.cols + a.requests, each = tiles * a.requests;
-        const int64_t busy = (each < all ? each : all) * heads, least = 512;
+        const int64_t busy = tiles * heads, least = 512;
         const int64_t steps = (a.max_keys + least - 1) / least;
         int64_t chunks = 256 / busy;  // one filling of the compute units
         chunks = chunks > steps ? steps : chunks;
@@ -530,7 +490,7 @@ AttnPlan attn_plan(const bq_attn &a)
         stride = stride > p.many.chunks ? stride : p.many.chunks;
     }
     p.stride = (int)stride;
-    p.work_bytes = p.stride > 1 ? a.tokens * a.q_heads * p.stride * (4 * (int64_t)a.cache.dim + 8) : 0;
+    p.work_bytes = p.stride > 1 ? a.tokens * a.q_heads * p.stride * (4 * (int64_t)a.cache.dim + 8) + 16 : 0;
     return p;
 }
 

@@ -50,27 +50,30 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
     const auto &sp = g.p.many;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c32 = lane & 31, half = lane >> 5;
-    const int b = blockIdx.z, kh = blockIdx.x;
-    const Request rq = request_at(a, b);
-    const int64_t rows64 = (int64_t)rq.n * g.group;
-    if (rq.n <= 0 || has_few(g.p, (int)rows64))
-        return;
-    const int rows = (int)rows64;
-    // the last tile first: it sees the most keys
-    const int tiles = (rows + ROWS - 1) / ROWS;
-    const int turn = blockIdx.y / sp.chunks, chunk = blockIdx.y % sp.chunks;
+    const int kh = blockIdx.x;
+    const int chunk = blockIdx.y % sp.chunks;
     const int P = a.cache.page, pmask = P - 1;
     const int64_t page_elems = ((int64_t)a.cache.heads << g.page_log2) * D;
     const T *kbase = static_cast<const T *>(a.cache.k) + (int64_t)kh * P * D;
     const T *vbase = static_cast<const T *>(a.cache.v) + (int64_t)kh * D * P;
-    const int32_t *table = a.table + (int64_t)b * a.ld_table;
 
     // staging: a thread's pieces are piece kc of rows kr + KROWS i (keys) and piece vc of rows vr + VROWS i (values)
     const int kc = threadIdx.x % KC, kr = threadIdx.x / KC;
     const int vc = threadIdx.x % 8, vr = threadIdx.x / 8;
 
-    for (int u = turn; u < tiles; u += sp.tiles) {
-        const int r0 = (tiles - 1 - u) * ROWS;
+    auto tiles_of = [&](int i) {
+        int rows, keys;
+        lane_request(g, i, false, rows, keys);
+        return (rows + ROWS - 1) / ROWS;
+    };
+    Walk walk;
+    int b, within;
+    for (int item = blockIdx.y / sp.chunks; find_item(walk, a.requests, item, b, within, tiles_of); item += sp.tiles) {
+        const Request rq = request_at(a, b);
+        const int32_t *table = a.table + (int64_t)b * a.ld_table;
+        const int rows = rq.n * g.group;
+        // the last tile first: it sees the most keys
+        const int r0 = ((rows + ROWS - 1) / ROWS - 1 - within) * ROWS;
         const int r = r0 + wave * 32 + c32;
         const bool live = r < rows;
         const int i_tok = live ? r / g.group : 0, hq = kh * g.group + (live ? r % g.group : 0);
@@ -250,8 +253,6 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
         }
         // ---- out, or this chunk's part of it
         l = across32(l, Add());
-        if (!live)
-            continue;
         const int64_t tok = rq.row0 + i_tok, row = tok * a.q_heads + hq;
         const float f = sp.chunks > 1 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
@@ -263,7 +264,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     v[e] = o[d][4 * q + e] * f;
-                if (sp.chunks > 1) {
+                if (!live) {
+                } else if (sp.chunks > 1) {
                     *reinterpret_cast<f32x4 *>(part_sums(g, row, chunk, D) + at) = v;
                 } else if constexpr (F32) {
                     *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + tok * a.ld_out + (int64_t)hq * D + at) = v;
@@ -276,7 +278,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
                     *reinterpret_cast<tx4 *>(static_cast<T *>(a.out) + tok * a.ld_out + (int64_t)hq * D + at) = x;
                 }
             }
-        if (sp.chunks > 1 && half == 0)
+        if (live && sp.chunks > 1 && half == 0)
             *part_stats(g, row, chunk, D) = make_float2(m, l);
     }
 }
@@ -295,7 +297,7 @@ static void tiles_dim(const AttnArgs &g, dim3 grid, hipStream_t st)
 hipError_t launch_attn_tiles(const AttnArgs &g, hipStream_t st)
 {
     const bq_attn &a = g.a;
-    const dim3 grid((unsigned)a.cache.heads, (unsigned)(g.p.many.tiles * g.p.many.chunks), (unsigned)a.requests);
+    const dim3 grid((unsigned)a.cache.heads, (unsigned)(g.p.many.tiles * g.p.many.chunks));
     if (a.cache.type == BQ_F16)
         a.cache.dim == 64 ? tiles_dim<BQ_F16, 64>(g, grid, st) : tiles_dim<BQ_F16, 128>(g, grid, st);
     else

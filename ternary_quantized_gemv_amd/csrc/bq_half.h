@@ -130,6 +130,46 @@ __device__ __forceinline__ int uniform_word(const int32_t *p)
 // Sizes in bytes of the three types.
 inline int type_size(int type) { return type == BQ_F32 ? 4 : 2; }
 
+// The items of all requests in a row: request i has count(i) of them, and a
+// workgroup asks for items in increasing order (item, item + grid, ...).  Each
+// lane counts one request of 64 at a time; nothing is read twice unless it has to.
+struct Walk {
+    int base = 0;    // the first of the 64 requests in hand
+    int before = 0;  // items of the requests in front of them
+    int mine = 0, upto = 0;
+    bool ready = false;
+};
+// Request b that has the item, and its number there; false behind the last one.
+// The same in all lanes.
+template <class COUNT>
+__device__ __forceinline__ bool find_item(Walk &w, int requests, int item, int &b, int &within, COUNT count)
+{
+    const int lane = threadIdx.x & 63;
+    for (; w.base < requests; w.base += 64, w.ready = false) {
+        if (!w.ready) {
+            w.mine = w.base + lane < requests ? count(w.base + lane) : 0;
+            w.upto = w.mine;
+            if (requests > 1) {
+#pragma unroll
+                for (int off = 1; off < 64; off <<= 1) {
+                    const int x = __shfl_up(w.upto, off, 64);
+                    w.upto += lane >= off ? x : 0;
+                }
+            }
+            w.ready = true;
+        }
+        const unsigned long long has = __ballot(item - w.before < w.upto);
+        if (has) {
+            const int at = __builtin_ctzll(has);
+            b = w.base + at;
+            within = item - w.before - (__builtin_amdgcn_readlane(w.upto, at) - __builtin_amdgcn_readlane(w.mine, at));
+            return true;
+        }
+        w.before += requests > 1 ? __builtin_amdgcn_readlane(w.upto, 63) : 0;
+    }
+    return false;
+}
+
 // The request that row t belongs to, of n requests with rows cu[b] ..
 // cu[b+1] - 1: the last b with cu[b] <= t (requests without rows are skipped
 // by it); n or more, or -1, where no request has the row.

@@ -27,8 +27,8 @@ hipError_t launch_append(const bq_append &a, hipStream_t st);
 // (few.cols of one key head's queries a tile) cuts the keys of all requests
 // into about few.items pieces per key head, at most `stride` per row, on the
 // device, where the lengths are known; few.grid workgroups per key head walk
-// them.  The kernel for many rows (many.cols a tile, many.tiles of them at
-// most per request, 0: not launched) takes many.chunks pieces of many.chunk
+// them.  The kernel for many rows (many.cols a tile, workgroups for many.tiles
+// of them per key head, 0: not launched) takes many.chunks pieces of many.chunk
 // keys.  The joins add the pieces up.
 struct AttnPlan {
     struct {

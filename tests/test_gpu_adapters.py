@@ -73,6 +73,15 @@ def test_adapters_bound_only_splits_the_work():
     assert all(o is not None for o in outs)
 
 
+def test_adapters_many_requests():
+    """More requests than a wavefront has lanes: one row each, and up to forty."""
+    import random
+    r = random.Random(1)
+    ids = [r.randint(-1, 3) for _ in range(150)]
+    run([r.randint(0, 2) for _ in ids], ids, 264, 70, 16, 4, "f32", "bf16")
+    run([r.choice((0, 1, 2, 40)) for _ in ids], ids, 264, 70, 16, 4, "f32", "f16")
+
+
 @pytest.mark.parametrize("size", [1e-20, 1e6, 1e15])
 def test_adapters_f32_rows_of_any_size(size):
     """x far outside f16's range through f16 adapters."""

@@ -99,6 +99,26 @@ def test_bounds_only_split_the_work(type, cache):
 
 
 @pytest.mark.parametrize("type,cache", TYPES)
+def test_more_rows_than_max_new_says(type, cache):
+    """Enough for the kernel of many rows, but a fraction of the true counts:
+    its workgroups walk several tiles each, of several requests."""
+    check([600, 3, 40, 700], [600, 300, 900, 1100], 8, 2, 64, type, cache, 16, 45, max_new=20, max_keys=64)
+
+
+@pytest.mark.parametrize("type,cache", [("f32", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("requests", [65, 130, 300])
+def test_many_requests(type, cache, requests):
+    """More requests than a wavefront has lanes, decode tokens and chunks among
+    each other, some empty."""
+    import random
+    r = random.Random(requests)
+    keys = [r.choice((0, 1, 17, 64, 300, r.randint(1, 2000))) for _ in range(requests)]
+    check([r.choice((0, 1, 1, 1)) for _ in keys], keys, 4, 2, 64, type, cache, 16, 46)
+    new = [r.choice((0, 1, 1, 5, 40)) for _ in keys]
+    check(new, [max(k, n) for k, n in zip(keys, new)], 4, 2, 64, type, cache, 32, 47)
+
+
+@pytest.mark.parametrize("type,cache", TYPES)
 def test_strides_and_wide_tables(type, cache):
     check([2, 33], [100, 250], 6, 2, 64, type, cache, 16, 51, pad=64, cols=40)
 
