@@ -342,7 +342,7 @@ int bq_read_floor(const void *p, int64_t bytes, uint32_t *sink, bq_stream s);
  * x, res, h, w and y hold `type`; rows are ld_* elements apart.  res, h and
  * y may be NULL (absent); h and y may each be x or res (same pointer and
  * leading dimension), and not otherwise overlap them.  n is a multiple of
- * qa, at most BQ_NORM_MAX; qa is 32, 64 or 128; eps > 0.  x, res, h, y and w
+ * qa, at most BQ_NORM_MAX; qa is 32, 64 or 128; eps >= 1e-30.  x, res, h, y and w
  * are 16-byte aligned, their leading dimensions (and ld_q) multiples of 16
  * bytes; q is 8-byte aligned with ld_q a multiple of 16, d 4-byte.  tokens =
  * 0 does nothing.  Non-finite values are outside the contract, as in the
@@ -457,9 +457,10 @@ int bq_kv_append(const bq_append *a, bq_stream s);
  * in the kernel: rows past `tokens`, keys past table_cols * page and pages
  * outside the cache are not read (keys of such a page count as unseen).
  * Places of keys below L must hold finite values; others may hold anything.
- * work (device, 16-byte aligned, bq_paged_attn_work_bytes bytes, may be NULL
- * if that is 0) is scratch of this call until it has run: calls that may run
- * at the same time need one each.  out must not overlap q.  tokens = 0 or
+ * work (device, 16-byte aligned, bq_paged_attn_work_bytes bytes -- some tens
+ * of megabytes at most, whatever the tokens and keys -- may be NULL if that is
+ * 0) is scratch of this call until it has run: calls that may run at the same
+ * time need one each.  out must not overlap q.  tokens = 0 or
  * requests = 0 does nothing.  Returns BQ_EARG / BQ_EALIGN before any launch,
  * or BQ_EHIP.  Allocates nothing.  Asynchronous on s. */
 typedef struct bq_attn {

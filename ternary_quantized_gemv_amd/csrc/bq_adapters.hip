@@ -35,12 +35,12 @@ template <int TOKENS>
 __device__ __forceinline__ bool adapter_item(const AdapterArgs &g, Walk &w, int item, int &b, int &first, int &end)
 {
     const bq_adapters &a = g.a;
-    int within = 0;
+    int within = 0, front;
     if (g.direct) {
         if (item >= a.requests)
             return false;
         b = item;
-    } else if (!find_item(w, a.requests, item, b, within, [&](int i) {
+    } else if (!find_item<false>(w, a.requests, item, b, within, front, [&](int i, int &) {
                    const int lo = a.cu[i], hi = a.cu[i + 1] > a.tokens ? (int)a.tokens : a.cu[i + 1];
                    return lo < 0 || hi < lo ? 0 : (hi - lo + TOKENS - 1) / TOKENS;
                })) {

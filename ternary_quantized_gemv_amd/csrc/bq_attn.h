@@ -167,23 +167,36 @@ __device__ __forceinline__ float load_query(const bq_attn &a, int64_t at, int st
     return factor;
 }
 
-// Where chunk c of row `row` (token * q_heads + head) keeps its part: D sums,
-// then, behind all rows' sums, a maximum and a sum of weights.
-__device__ __forceinline__ float *part_sums(const AttnArgs &g, int64_t row, int c, int dim)
+// A row's place in a piece: its D sums, and its maximum and sum of weights.
+struct Part {
+    float *sums;
+    float2 *stats;
+};
+// Few rows: row `row` of piece `piece` (2 few.items of them per key head).
+__device__ __forceinline__ Part few_part(const AttnArgs &g, int dim, int kh, int piece, int row)
 {
-    return static_cast<float *>(g.a.work) + (row * g.p.stride + c) * dim;
+    const int64_t at = ((int64_t)kh * 2 * g.p.few.items + piece) * g.p.few.cols + row;
+    char *w = static_cast<char *>(g.a.work);
+    return Part{reinterpret_cast<float *>(w) + at * dim, reinterpret_cast<float2 *>(w + g.p.few_stats) + at};
 }
-__device__ __forceinline__ float2 *part_stats(const AttnArgs &g, int64_t row, int c, int dim)
+// Many rows: row `row` of a tile, the sums chunk by chunk, a row's statistics
+// next to each other (one lane reads all of them).
+__device__ __forceinline__ Part many_part(const AttnArgs &g, int dim, int kh, int tile, int chunk, int row)
 {
-    float *end = static_cast<float *>(g.a.work) + g.a.tokens * g.a.q_heads * g.p.stride * dim;
-    return reinterpret_cast<float2 *>(end) + row * g.p.stride + c;
+    const int64_t tiles = (int64_t)kh * g.p.many.tiles + tile;
+    char *w = static_cast<char *>(g.a.work);
+    return Part{reinterpret_cast<float *>(w + g.p.many_sums) + ((tiles * g.p.many.chunks + chunk) * g.p.many.cols + row) * dim,
+                reinterpret_cast<float2 *>(w + g.p.many_stats) + (tiles * g.p.many.cols + row) * g.p.many.chunks + chunk};
 }
-// Behind those, the units of a piece of few rows' keys: the kernel leaves its
-// cut to the join.
-__device__ __forceinline__ int32_t *part_units(const AttnArgs &g, int dim)
+// What the kernels leave for the joins: the units of a piece of few rows' keys,
+// the first piece of each split request of few rows, and the first tile of
+// each request of many rows.
+__device__ __forceinline__ int32_t *note_units(const AttnArgs &g)
 {
-    return reinterpret_cast<int32_t *>(part_stats(g, g.a.tokens * g.a.q_heads, 0, dim));
+    return reinterpret_cast<int32_t *>(static_cast<char *>(g.a.work) + g.p.notes);
 }
+__device__ __forceinline__ int32_t *note_piece(const AttnArgs &g, int b) { return note_units(g) + 4 + b; }
+__device__ __forceinline__ int32_t *note_tile(const AttnArgs &g, int b) { return note_units(g) + 4 + g.a.requests + b; }
 
 hipError_t launch_attn_tiles(const AttnArgs &g, hipStream_t st);
 

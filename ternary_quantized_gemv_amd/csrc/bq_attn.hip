@@ -38,7 +38,7 @@ constexpr int kMaxChunks = 128; // pieces of a row's keys that the joins take
 // among them: 75 us against 61 for 32 requests of 3 to 8192 keys), so every
 // workgroup derives the same equal cut from the lengths: units of 128 keys,
 // `chunk` of them a piece, so that the pieces are about few.items per key head
-// and at most g.p.stride per row.
+// and at most kMaxChunks per row.
 
 // Tiles of rows and units of keys; a request without keys has one piece, of zeros.
 __device__ __forceinline__ int few_tiles(const AttnArgs &g, int rows) { return (rows + g.p.few.cols - 1) / g.p.few.cols; }
@@ -55,16 +55,23 @@ __device__ __forceinline__ float wave_sum(float x)
 // Units of a piece: those of all requests over the pieces wanted, and, as every
 // request rounds its pieces up, more where that made too many (twice: pieces
 // that fill the GPU once and a third take as long as two fillings; not for so
-// many requests that they even out).  Sums in f32: the same in every
-// workgroup, and exact enough.
+// many requests that they even out).  The sums are f32, the same in every
+// workgroup and within 2^-13 (at most 1024 + 6 additions): with at most 1536
+// places, the split pieces stay below 2 few.items + 1/2, so within them.
 __device__ __forceinline__ int few_chunk(const AttnArgs &g)
 {
     const int lane = threadIdx.x & 63;
     const float want = (float)g.p.few.items;
     float total = 0.0f;
     int most = 1, tiles = 0, units = 1;
+    if (g.a.requests == 1) {  // a single token waits for every load in a row: scalar ones, and few
+        const Request rq = request_at(g.a, 0);
+        tiles = rq.n > 0 && has_few(g.p, rq.n * g.group) ? few_tiles(g, rq.n * g.group) : 0;
+        most = few_units(rq.keys);
+        total = (float)tiles * (float)most;
+    }
 #pragma unroll 4
-    for (int base = 0; base < g.a.requests; base += 64) {
+    for (int base = 0; base < g.a.requests && g.a.requests > 1; base += 64) {
         int rows = 0, keys = 0;
         if (base + lane < g.a.requests)
             lane_request(g, base + lane, true, rows, keys);
@@ -79,16 +86,16 @@ __device__ __forceinline__ int few_chunk(const AttnArgs &g)
         for (int off = 1; off < 64; off <<= 1)
             most = max(most, __shfl_xor(most, off, 64));
     }
-    const int least = max((most + g.p.stride - 1) / g.p.stride, 1);
+    const int least = (most + kMaxChunks - 1) / kMaxChunks;
     int chunk = max((int)fminf(__builtin_ceilf(total / want), 16777216.0f), least);
     if (g.a.requests > 1 && g.a.requests <= 64) {
         for (int again = 0; again < 2; ++again) {
             const float count = wave_sum((float)(tiles * ((units + chunk - 1) / chunk)));
             if (count > want)
-                chunk = min(max((int)fminf(__builtin_ceilf((float)chunk * (count / want)), 16777216.0f), chunk + 1), max(most, least));
+                chunk = max(min((int)fminf(__builtin_ceilf((float)chunk * (count / want)), 16777216.0f), most), chunk);
         }
     }
-    return __builtin_amdgcn_readfirstlane(chunk);
+    return __builtin_amdgcn_readfirstlane(g.p.few.split ? chunk : max(chunk, most));
 }
 
 // CW of the W wavefronts take 16 NT columns each, the others the same columns
@@ -116,21 +123,34 @@ __global__ __launch_bounds__(64 * W, NT == 1 && !F32 ? 3 : 2) void attn_kernel(c
     const T *kbase = static_cast<const T *>(a.cache.k) + (int64_t)kh * P * D + 8 * q4 + (c16 & 3) * D;
     const T *vbase = static_cast<const T *>(a.cache.v) + (int64_t)(kh * D + c16) * P;
     const int chunk_units = few_chunk(g);
-    if (g.p.stride > 1 && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-        *part_units(g, D) = chunk_units;
-    auto pieces = [&](int i) {
+    if (g.p.few.split && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+        *note_units(g) = chunk_units;
+    // the pieces of all requests, and those of split ones, which have places in the scratch
+    auto pieces = [&](int i, int &placed) {
         int rows, keys;
         lane_request(g, i, true, rows, keys);
-        return few_tiles(g, rows) * ((few_units(keys) + chunk_units - 1) / chunk_units);
+        const int chunks = (few_units(keys) + chunk_units - 1) / chunk_units, n = few_tiles(g, rows) * chunks;
+        placed = chunks > 1 ? n : 0;
+        return n;
     };
     Walk walk;
-    int b, within;
-    for (int item = blockIdx.y; find_item(walk, a.requests, item, b, within, pieces); item += gridDim.y) {
+    int b = 0, within = 0, front = 0;
+    auto find = [&](int item) {
+        if (a.requests > 1)
+            return find_item<true>(walk, a.requests, item, b, within, front, pieces);
+        const Request rq = request_at(a, 0);
+        const int rows = rq.n > 0 && has_few(g.p, rq.n * g.group) ? rq.n * g.group : 0;
+        within = item;
+        return item < few_tiles(g, rows) * ((few_units(rq.keys) + chunk_units - 1) / chunk_units);
+    };
+    for (int item = blockIdx.y; find(item); item += gridDim.y) {
         const Request rq = request_at(a, b);
         const int rows = rq.n * g.group, tiles = few_tiles(g, rows), units = few_units(rq.keys);
         // a request's pieces are as even as its units allow
         const int chunks = (units + chunk_units - 1) / chunk_units, keys = (units + chunks - 1) / chunks * kAttnStep;
         const int chunk = within / tiles, r0 = (within - chunk * tiles) * COLS;
+        if (chunks > 1 && kh == 0 && within == 0 && threadIdx.x == 0)
+            *note_piece(g, b) = front;
         const int32_t *table = a.table + (int64_t)b * a.ld_table;
         // ---- the keys: those that the tile's last row sees, this workgroup's chunk of them
         const int last_row = min(r0 + COLS, rows) - 1;
@@ -310,9 +330,10 @@ __global__ __launch_bounds__(64 * W, NT == 1 && !F32 ? 3 : 2) void attn_kernel(c
                 else
                     store8(static_cast<T *>(a.out) + at, v);
             } else {
-                store8(part_sums(g, tok * a.q_heads + hq, chunk, D) + d8, v);
+                const Part part = few_part(g, D, kh, front + within, cr);
+                store8(part.sums + d8, v);
                 if (d8 == 0)
-                    *part_stats(g, tok * a.q_heads + hq, chunk, D) = make_float2(mt, lt);
+                    *part.stats = make_float2(mt, lt);
             }
         }
         __syncthreads();
@@ -330,30 +351,35 @@ __global__ __launch_bounds__(256) void attn_join_few(const AttnArgs g)
     __shared__ float weight[kMaxChunks];
     __shared__ float so[GROUPS][D + 4];
     const int lane = threadIdx.x & 63;
+    // all that the rest hangs on in one go (notes of a request that has none are not used)
+    const int chunk_units = uniform_word(note_units(g)), first = uniform_word(note_piece(g, blockIdx.y));
     const Request rq = request_at(a, blockIdx.y);
+    asm volatile("" ::"s"(chunk_units), "s"(first));
     const int64_t rows64 = (int64_t)rq.n * g.group;
     if (rq.n <= 0 || !has_few(g.p, (int)rows64) || (int64_t)blockIdx.x >= (int64_t)rq.n * a.q_heads)
         return;
-    const int chunk_units = uniform_word(part_units(g, D));
     const int chunks = (few_units(rq.keys) + chunk_units - 1) / chunk_units;
     if (chunks <= 1)
         return;
+    const int tiles = few_tiles(g, (int)rows64);
     const int grp = threadIdx.x / L, d8 = threadIdx.x % L * 8;
     for (int64_t u = blockIdx.x; u < (int64_t)rq.n * a.q_heads; u += gridDim.x) {
-        const int64_t row = (int64_t)rq.row0 * a.q_heads + u;
+        // row i G + g of key head kh: tile and row of the tile; its pieces are `tiles` apart
+        const int i = (int)(u / a.q_heads), hq = (int)(u - (int64_t)i * a.q_heads), kh = hq / g.group;
+        const int r = i * g.group + hq - kh * g.group, tile = r / g.p.few.cols, cr = r - tile * g.p.few.cols;
         const float2 none = make_float2(kNone, 0.0f);
         // all loads first: a single token waits for little else
         float v[MOST][8];
 #pragma unroll
-        for (int i = 0; i < MOST; ++i) {
+        for (int k = 0; k < MOST; ++k) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[i][e] = 0.0f;
-            if (grp + GROUPS * i < chunks)
-                load8(part_sums(g, row, grp + GROUPS * i, D) + d8, v[i]);
+                v[k][e] = 0.0f;
+            if (grp + GROUPS * k < chunks)
+                load8(few_part(g, D, kh, first + (grp + GROUPS * k) * tiles + tile, cr).sums + d8, v[k]);
         }
-        const float2 s0 = lane < chunks ? *part_stats(g, row, lane, D) : none;
-        const float2 s1 = lane + 64 < chunks ? *part_stats(g, row, lane + 64, D) : none;
+        const float2 s0 = lane < chunks ? *few_part(g, D, kh, first + lane * tiles + tile, cr).stats : none;
+        const float2 s1 = lane + 64 < chunks ? *few_part(g, D, kh, first + (lane + 64) * tiles + tile, cr).stats : none;
         float m = fmaxf(s0.x, s1.x);
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1)
@@ -371,11 +397,11 @@ __global__ __launch_bounds__(256) void attn_join_few(const AttnArgs g)
         __syncthreads();
         float o[8] = {};
 #pragma unroll
-        for (int i = 0; i < MOST; ++i) {
-            const float f = weight[grp + GROUPS * i];  // 0 where there is no piece
+        for (int k = 0; k < MOST; ++k) {
+            const float f = weight[grp + GROUPS * k];  // 0 where there is no piece
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                o[e] = __builtin_fmaf(v[i][e], f, o[e]);
+                o[e] = __builtin_fmaf(v[k][e], f, o[e]);
         }
         store8(&so[grp][d8], o);
         __syncthreads();
@@ -392,7 +418,7 @@ __global__ __launch_bounds__(256) void attn_join_few(const AttnArgs g)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 o[e] *= inv;
-            store8(static_cast<OT *>(a.out) + row / a.q_heads * a.ld_out + row % a.q_heads * D + d8, o);
+            store8(static_cast<OT *>(a.out) + (int64_t)(rq.row0 + i) * a.ld_out + (int64_t)hq * D + d8, o);
         }
         __syncthreads();
     }
@@ -417,8 +443,15 @@ __global__ __launch_bounds__(256) void attn_join_many(const AttnArgs g)
     const int64_t n = lo < 0 ? 0 : (hi > a.tokens ? a.tokens : hi) - lo;
     if (n <= 0 || has_few(g.p, (int)(n * g.group)))
         return;
-    const float *sums = part_sums(g, row, 0, D) + d8;
-    const float2 *stats = part_stats(g, row, 0, D);
+    // the row's tile, counted from the request's last, and its row there; tiles past the scratch are not split
+    const int hq = (int)(row - tok * a.q_heads), kh = hq / g.group, cols = g.p.many.cols;
+    const int r = (int)(tok - lo) * g.group + hq - kh * g.group, tiles = ((int)n * g.group + cols - 1) / cols;
+    const int tile = *note_tile(g, b) + tiles - 1 - r / cols;
+    if (tile >= g.p.many.tiles)
+        return;
+    const Part first = many_part(g, D, kh, tile, 0, r % cols);  // the next chunk's sums are cols rows on
+    const float *sums = first.sums + d8;
+    const float2 *stats = first.stats;
     float m = kNone;
     for (int c = 0; c < chunks; ++c)
         m = fmaxf(m, stats[c].x);
@@ -426,10 +459,11 @@ __global__ __launch_bounds__(256) void attn_join_many(const AttnArgs g)
     float l = 0.0f, o[8] = {};
 #pragma unroll 4
     for (int c = 0; c < chunks; ++c) {
-        const float f = __builtin_amdgcn_exp2f(stats[c].x - m);
+        const float2 st = stats[c];
+        const float f = __builtin_amdgcn_exp2f(st.x - m);
         float v[8];
-        load8(sums + (int64_t)c * D, v);
-        l = __builtin_fmaf(stats[c].y, f, l);
+        load8(sums + (int64_t)c * cols * D, v);
+        l = __builtin_fmaf(st.y, f, l);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             o[e] = __builtin_fmaf(v[e], f, o[e]);
@@ -438,7 +472,7 @@ __global__ __launch_bounds__(256) void attn_join_many(const AttnArgs g)
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         o[e] *= inv;
-    store8(static_cast<OT *>(a.out) + tok * a.ld_out + (row - tok * a.q_heads) * D + d8, o);
+    store8(static_cast<OT *>(a.out) + tok * a.ld_out + (int64_t)hq * D + d8, o);
 }
 
 AttnPlan attn_plan(const bq_attn &a)
@@ -447,10 +481,11 @@ AttnPlan attn_plan(const bq_attn &a)
     const int64_t group = a.q_heads / a.cache.heads, heads = a.cache.heads;
     const int64_t most = a.max_new < a.tokens ? a.max_new : a.tokens;
     const int64_t rows = most * group;
-    p.few.cols = p.few.grid = p.few.items = 0;
+    p.few.cols = p.few.grid = p.few.items = p.few.split = 0;
     p.many.cols = p.many.tiles = p.many.chunk = 0;
     p.many.chunks = 1;
-    int64_t stride = 1;
+    const int64_t row_bytes = 4 * (int64_t)a.cache.dim;
+    int64_t few_rows = 0, many_rows = 0;  // of the scratch
     if (rows <= kFewRows || a.requests > 1) {  // one request of many rows: one kernel
         p.few.cols = rows <= 16 || rows > kFewRows ? 16 : rows <= 32 ? 32 : 64;
         const int64_t tiles = ((rows > kFewRows ? kFewRows : rows) + p.few.cols - 1) / p.few.cols;
@@ -460,9 +495,6 @@ AttnPlan attn_plan(const bq_attn &a)
         const int64_t want = p.few.cols == 64 ? 256 : p.few.cols == 16 && a.type != BQ_F32 ? 768 : 512;
         const int64_t items = want / heads < 1 ? 1 : want / heads;
         const int64_t cut = units < 1 ? 1 : units, each = tiles * a.requests;
-        // no row has more pieces than units, nor than the items if they are all its own
-        stride = cut < items ? cut : items;
-        stride = stride > kMaxChunks ? kMaxChunks : stride;
         // a workgroup for every piece there can be; of more than 64 requests two fillings of the GPU, which look
         // the requests up once and walk their pieces
         int64_t grid = items + each < each * cut ? items + each : each * cut;
@@ -470,6 +502,8 @@ AttnPlan attn_plan(const bq_attn &a)
             grid = 2 * items;
         p.few.items = (int)items;
         p.few.grid = (int)(grid > 65535 ? 65535 : grid);
+        p.few.split = cut > 1;
+        few_rows = p.few.split ? heads * 2 * items * p.few.cols : 0;
     }
     if (rows > kFewRows) {
         p.many.cols = rows <= 128 || a.type == BQ_F32 ? 128 : 256;
@@ -483,14 +517,17 @@ AttnPlan attn_plan(const bq_attn &a)
         const int64_t steps = (a.max_keys + least - 1) / least;
         int64_t chunks = 256 / busy;  // one filling of the compute units
         chunks = chunks > steps ? steps : chunks;
-        chunks = chunks > kMaxChunks ? kMaxChunks : chunks < 1 ? 1 : chunks;
+        chunks = chunks < 1 ? 1 : chunks;
         const int64_t per = steps < 1 ? 1 : (steps + chunks - 1) / chunks;
         p.many.chunk = (int)(per * least);
         p.many.chunks = (int)(steps < 1 ? 1 : (steps + per - 1) / per);
-        stride = stride > p.many.chunks ? stride : p.many.chunks;
+        many_rows = p.many.chunks > 1 ? heads * p.many.tiles * p.many.chunks * p.many.cols : 0;
     }
-    p.stride = (int)stride;
-    p.work_bytes = p.stride > 1 ? a.tokens * a.q_heads * p.stride * (4 * (int64_t)a.cache.dim + 8) + 16 : 0;
+    p.few_stats = few_rows * row_bytes;
+    p.many_sums = p.few_stats + few_rows * 8;
+    p.many_stats = p.many_sums + many_rows * row_bytes;
+    p.notes = p.many_stats + many_rows * 8;
+    p.work_bytes = few_rows || many_rows ? p.notes + 16 + 8 * (int64_t)a.requests : 0;
     return p;
 }
 
@@ -515,7 +552,7 @@ template <class OT, int D>
 static void join_type(const AttnArgs &g, hipStream_t st)
 {
     const bq_attn &a = g.a;
-    if (g.p.few.cols && g.p.stride > 1) {
+    if (g.p.few.split) {
         const int64_t rows = (a.max_new < a.tokens ? a.max_new : a.tokens) * (a.q_heads / a.cache.heads);
         const int64_t most = (rows < kFewRows ? rows : kFewRows) * a.cache.heads;
         hipLaunchKernelGGL((attn_join_few<OT, D>), dim3((unsigned)most, (unsigned)a.requests), dim3(256), 0, st, g);
@@ -552,7 +589,7 @@ hipError_t launch_attn(const bq_attn &a, const AttnPlan &p, hipStream_t st)
         else
             wide ? attn_dim<BQ_BF16, 128>(g, grid, st) : attn_dim<BQ_BF16, 64>(g, grid, st);
     }
-    if (p.stride > 1) {
+    if (p.few.split || p.many.chunks > 1) {
         if (f16)
             wide ? join_dim<BQ_F16, 128>(g, st) : join_dim<BQ_F16, 64>(g, st);
         else

@@ -61,14 +61,14 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
     const int kc = threadIdx.x % KC, kr = threadIdx.x / KC;
     const int vc = threadIdx.x % 8, vr = threadIdx.x / 8;
 
-    auto tiles_of = [&](int i) {
+    auto tiles_of = [&](int i, int &) {
         int rows, keys;
         lane_request(g, i, false, rows, keys);
         return (rows + ROWS - 1) / ROWS;
     };
     Walk walk;
-    int b, within;
-    for (int item = blockIdx.y / sp.chunks; find_item(walk, a.requests, item, b, within, tiles_of); item += sp.tiles) {
+    int b, within, front;
+    for (int item = blockIdx.y / sp.chunks; find_item<false>(walk, a.requests, item, b, within, front, tiles_of); item += sp.tiles) {
         const Request rq = request_at(a, b);
         const int32_t *table = a.table + (int64_t)b * a.ld_table;
         const int rows = rq.n * g.group;
@@ -91,8 +91,14 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
 
         const int last_row = min(r0 + ROWS, rows) - 1;
         const int seen = min(rq.keys, rq.keys - rq.n + last_row / g.group + 1);
+        // tiles past those that the launch and its scratch were made for are not split
+        const bool split = sp.chunks > 1 && item < sp.tiles;
+        if (sp.chunks > 1 && kh == 0 && chunk == 0 && within == 0 && threadIdx.x == 0)
+            *note_tile(g, b) = item;
+        if (!split && chunk)
+            continue;
         const int begin = chunk * sp.chunk;
-        const int end = chunk == sp.chunks - 1 ? seen : min(seen, begin + sp.chunk);
+        const int end = !split || chunk == sp.chunks - 1 ? seen : min(seen, begin + sp.chunk);
         const int first_last = rq.keys - rq.n + r0 / g.group;
 
         // ---- staging of one tile: pages (one tile ahead), memory to registers, registers to LDS
@@ -253,8 +259,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
         }
         // ---- out, or this chunk's part of it
         l = across32(l, Add());
-        const int64_t tok = rq.row0 + i_tok, row = tok * a.q_heads + hq;
-        const float f = sp.chunks > 1 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+        const int64_t tok = rq.row0 + i_tok;
+        const Part part = many_part(g, D, kh, split ? item : 0, chunk, wave * 32 + c32);
+        const float f = split ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -265,8 +272,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
                 for (int e = 0; e < 4; ++e)
                     v[e] = o[d][4 * q + e] * f;
                 if (!live) {
-                } else if (sp.chunks > 1) {
-                    *reinterpret_cast<f32x4 *>(part_sums(g, row, chunk, D) + at) = v;
+                } else if (split) {
+                    *reinterpret_cast<f32x4 *>(part.sums + at) = v;
                 } else if constexpr (F32) {
                     *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + tok * a.ld_out + (int64_t)hq * D + at) = v;
                 } else {
@@ -278,8 +285,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
                     *reinterpret_cast<tx4 *>(static_cast<T *>(a.out) + tok * a.ld_out + (int64_t)hq * D + at) = x;
                 }
             }
-        if (live && sp.chunks > 1 && half == 0)
-            *part_stats(g, row, chunk, D) = make_float2(m, l);
+        if (live && split && half == 0)
+            *part.stats = make_float2(m, l);
     }
 }
 

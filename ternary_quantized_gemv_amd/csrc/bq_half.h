@@ -130,42 +130,45 @@ __device__ __forceinline__ int uniform_word(const int32_t *p)
 // Sizes in bytes of the three types.
 inline int type_size(int type) { return type == BQ_F32 ? 4 : 2; }
 
-// The items of all requests in a row: request i has count(i) of them, and a
-// workgroup asks for items in increasing order (item, item + grid, ...).  Each
-// lane counts one request of 64 at a time; nothing is read twice unless it has to.
+// The items of all requests in a row: request i has count(i, other) of them,
+// and a workgroup asks for items in increasing order (item, item + grid, ...).
+// Each lane counts one request of 64 at a time.  `other` is a second number
+// that is added up beside the items.  Between two items only these are kept
+// (scalars: the registers of a workgroup at work are its products').
 struct Walk {
-    int base = 0;    // the first of the 64 requests in hand
-    int before = 0;  // items of the requests in front of them
-    int mine = 0, upto = 0;
-    bool ready = false;
+    int base = 0;                 // the first of the 64 requests in hand
+    int before = 0, before2 = 0;  // items (second numbers) of the requests in front of them
 };
-// Request b that has the item, and its number there; false behind the last one.
-// The same in all lanes.
-template <class COUNT>
-__device__ __forceinline__ bool find_item(Walk &w, int requests, int item, int &b, int &within, COUNT count)
+// Request b that has the item, its number there, and the second numbers of the
+// requests in front of b (TWO); false behind the last item.  The same in all lanes.
+template <bool TWO, class COUNT>
+__device__ __forceinline__ bool find_item(Walk &w, int requests, int item, int &b, int &within, int &front, COUNT count)
 {
     const int lane = threadIdx.x & 63;
-    for (; w.base < requests; w.base += 64, w.ready = false) {
-        if (!w.ready) {
-            w.mine = w.base + lane < requests ? count(w.base + lane) : 0;
-            w.upto = w.mine;
-            if (requests > 1) {
+    for (; w.base < requests; w.base += 64) {
+        int mine = 0, mine2 = 0;
+        if (w.base + lane < requests)
+            mine = count(w.base + lane, mine2);
+        int upto = mine, upto2 = mine2;
+        if (requests > 1) {
 #pragma unroll
-                for (int off = 1; off < 64; off <<= 1) {
-                    const int x = __shfl_up(w.upto, off, 64);
-                    w.upto += lane >= off ? x : 0;
-                }
+            for (int off = 1; off < 64; off <<= 1) {
+                const int x = __shfl_up(upto, off, 64), y = TWO ? __shfl_up(upto2, off, 64) : 0;
+                upto += lane >= off ? x : 0;
+                upto2 += lane >= off ? y : 0;
             }
-            w.ready = true;
         }
-        const unsigned long long has = __ballot(item - w.before < w.upto);
+        const unsigned long long has = __ballot(item - w.before < upto);
         if (has) {
             const int at = __builtin_ctzll(has);
             b = w.base + at;
-            within = item - w.before - (__builtin_amdgcn_readlane(w.upto, at) - __builtin_amdgcn_readlane(w.mine, at));
+            within = item - w.before - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at));
+            front = TWO ? w.before2 + __builtin_amdgcn_readlane(upto2, at) - __builtin_amdgcn_readlane(mine2, at) : 0;
             return true;
         }
-        w.before += requests > 1 ? __builtin_amdgcn_readlane(w.upto, 63) : 0;
+        w.before += __builtin_amdgcn_readlane(upto, requests > 1 ? 63 : 0);
+        if (TWO)
+            w.before2 += __builtin_amdgcn_readlane(upto2, requests > 1 ? 63 : 0);
     }
     return false;
 }

@@ -157,8 +157,9 @@ BQ_EXPORT int bq_rmsnorm_q8(const bq_norm *a, bq_stream s)
         return set_error(BQ_EARG, "%s: f16_scale %d is not 0 or 1", fn, (int)a->f16_scale);
     if (a->reserved != 0)
         return set_error(BQ_EARG, "%s: reserved must be 0", fn);
-    if (!(a->eps > 0.0) || !isfinite(a->eps))
-        return set_error(BQ_EARG, "%s: eps %g is not a positive number", fn, a->eps);
+    // below that, a zero row's 1 / sqrt(eps) would come near f32's range
+    if (!(a->eps >= 1e-30) || !isfinite(a->eps))
+        return set_error(BQ_EARG, "%s: eps %g is not a number of at least 1e-30", fn, a->eps);
     int rc = check_tokens(fn, a->tokens);
     if (rc)
         return rc;

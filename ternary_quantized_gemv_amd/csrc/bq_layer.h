@@ -24,17 +24,24 @@ hipError_t launch_norm(int type, const NormArgs &a, int64_t rows, hipStream_t st
 hipError_t launch_append(const bq_append &a, hipStream_t st);
 
 // How bq_paged_attn splits its work (attn_plan).  The kernel for few rows
-// (few.cols of one key head's queries a tile) cuts the keys of all requests
-// into about few.items pieces per key head, at most `stride` per row, on the
-// device, where the lengths are known; few.grid workgroups per key head walk
-// them.  The kernel for many rows (many.cols a tile, workgroups for many.tiles
-// of them per key head, 0: not launched) takes many.chunks pieces of many.chunk
-// keys.  The joins add the pieces up.
+// (few.cols of one key head's queries a tile, 0: not launched) cuts the keys of
+// all requests into about few.items pieces per key head on the device, where
+// the lengths are known (one piece a request with few.split 0); few.grid
+// workgroups per key head walk them.  The kernel for many rows (many.cols a
+// tile, workgroups for many.tiles of them per key head, 0: not launched) takes
+// many.chunks pieces of many.chunk keys.  The joins add the pieces up.
+//
+// Scratch: for the pieces of split requests, cols rows of dim sums each, then
+// their (maximum, sum of weights) pairs -- 2 few.items per key head: a request
+// in c >= 2 pieces has more than c / 2 times the keys of one, and all requests
+// have few.items times that -- and many.tiles * many.chunks; then notes of the
+// kernels to the joins.
 struct AttnPlan {
     struct {
-        int cols;  // 0: not launched
+        int cols;
         int grid;
         int items;
+        int split;
     } few;
     struct {
         int cols;
@@ -42,7 +49,7 @@ struct AttnPlan {
         int chunks;
         int chunk;
     } many;
-    int stride;  // places per row for the pieces
+    int64_t few_stats, many_sums, many_stats, notes;  // byte offsets in the scratch (few's sums at 0)
     int64_t work_bytes;
 };
 AttnPlan attn_plan(const bq_attn &a);

@@ -103,6 +103,9 @@ def test_more_rows_than_max_new_says(type, cache):
     """Enough for the kernel of many rows, but a fraction of the true counts:
     its workgroups walk several tiles each, of several requests."""
     check([600, 3, 40, 700], [600, 300, 900, 1100], 8, 2, 64, type, cache, 16, 45, max_new=20, max_keys=64)
+    # split over the keys as well: the tiles that the scratch has no place for are not
+    check([600, 3, 40, 700], [600, 300, 900, 5100], 8, 2, 64, type, cache, 16, 48, max_new=20, max_keys=4000)
+    check([900], [6000], 8, 2, 64, type, cache, 16, 49, max_new=20, max_keys=4000)
 
 
 @pytest.mark.parametrize("type,cache", [("f32", "bf16"), ("f16", "f16")])

@@ -101,6 +101,20 @@ def test_norm_extremes(f16_scale):
     check(x, t.zeros_like(x), w, 128, True, f16_scale)
 
 
+def test_norm_least_eps():
+    """Zero rows and rows of subnormal values at the smallest eps."""
+    t, bq = torch(), bqmod()
+    x = t.zeros(3, 128)
+    x[1] = 1e-42
+    x[2, 5] = -3e-39
+    w = t.ones(128)
+    q = t.empty(3, 128, dtype=t.int8, device="cuda")
+    d = t.empty(3, 1, device="cuda")
+    bq.bq_rmsnorm_q8(x.cuda(), w.cuda(), 1e-30, 128, q, d)
+    _, _, rq, rd = norm_ref(x, None, w, 1e-30, 128, False)
+    assert t.equal(q.cpu(), rq) and t.equal(d.cpu(), rd) and (rq[0] == 0).all()
+
+
 def test_norm_in_place():
     """h in place of the residual and y in place of x."""
     t, bq = torch(), bqmod()
