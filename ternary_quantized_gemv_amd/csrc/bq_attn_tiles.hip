@@ -9,9 +9,9 @@
 // l % 32, and operands hold k = 8 (l / 32) + e.  Row 8 a + 4 h + i of a 32-key
 // tile is assigned key 16 (a / 2) + 8 h + 4 (a % 2) + i, so that a lane's
 // registers 8 s .. 8 s + 7 are keys 16 s + 8 h .. + 7: the B operand of the
-// second product as they stand.  Both tiles lie in LDS in 16-byte pieces, piece
-// c of row r at c ^ (r % 8) of the row, so that the eight lanes that a read
-// serves at a time touch all banks once.
+// second product as they stand.  Both tiles lie in LDS in 16-byte pieces, turned
+// within their rows so that the 16 lanes that a read serves at a time (16
+// neighbouring rows) touch all 64 banks once.
 //
 // The running maximum is only raised when a tile's exceeds it by 2^8: until
 // then the weights are at most 2^8 times larger than they would be, which
@@ -26,6 +26,12 @@ namespace bq {
 
 constexpr int kTileKeys = 64;
 constexpr float kSlack = 8.0f;  // log2
+
+// Piece c of row r lies at c ^ turn(r) of its row of PIECES (16: one row fills
+// the banks; 8: two rows do).  (No bank conflicts are counted; with r % 8 for
+// both, every second read cycle was one.)
+template <int PIECES>
+__device__ __forceinline__ int turn(int r) { return PIECES == 16 ? r & 15 : (r >> 1) & 7; }
 
 template <int CT, int D, int WAVES, bool F32>
 __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnArgs g)
@@ -139,7 +145,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
 #pragma unroll
             for (int i = 0; i < KL; ++i) {
                 const int row = kr + KROWS * i;
-                ks[buf][row * KC + (kc ^ (row & 7))] = kreg[i];
+                ks[buf][row * KC + (kc ^ turn<KC>(row))] = kreg[i];
             }
             if (k0 + kTileKeys > end || bad) {
                 // places that no row sees may hold anything: their values must not meet a weight of 0
@@ -152,7 +158,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
 #pragma unroll
             for (int i = 0; i < VL; ++i) {
                 const int row = vr + VROWS * i;
-                vs[buf][row * 8 + (vc ^ (row & 7))] = vreg[i];
+                vs[buf][row * 8 + (vc ^ turn<8>(row))] = vreg[i];
             }
         };
 
@@ -184,7 +190,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
                     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int j = 0; j < DJ; ++j) {
-                    const v8 kf = ks[buf][krow * KC + ((2 * j + half) ^ (krow & 7))];
+                    const v8 kf = ks[buf][krow * KC + ((2 * j + half) ^ turn<KC>(krow))];
 #pragma unroll
                     for (int p = NP - 1; p >= 0; --p)
                         s = Num<CT>::mfma32(kf, qf[p][j], s);
@@ -241,7 +247,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attn_tiles(const AttnAr
                     const int row = 32 * d + c32;
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const v8 vf = vs[buf][row * 8 + ((4 * h + 2 * k + half) ^ (row & 7))];
+                        const v8 vf = vs[buf][row * 8 + ((4 * h + 2 * k + half) ^ turn<8>(row))];
 #pragma unroll
                         for (int p = NP - 1; p >= 0; --p)
                             o[d] = Num<CT>::mfma32(vf, pf[p][k], o[d]);
