@@ -44,14 +44,6 @@ constexpr int kMaxChunks = 128; // pieces of a row's keys that the joins take
 __device__ __forceinline__ int few_tiles(const AttnArgs &g, int rows) { return (rows + g.p.few.cols - 1) / g.p.few.cols; }
 __device__ __forceinline__ int few_units(int keys) { return keys > kAttnStep ? (keys + kAttnStep - 1) / kAttnStep : 1; }
 
-__device__ __forceinline__ float wave_sum(float x)
-{
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1)
-        x += __shfl_xor(x, off, 64);
-    return x;
-}
-
 // Units of a piece: those of all requests over the pieces wanted, and, as every
 // request rounds its pieces up, more where that made too many (twice: pieces
 // that fill the GPU once and a third take as long as two fillings; not for so
@@ -81,16 +73,14 @@ __device__ __forceinline__ int few_chunk(const AttnArgs &g)
         most = max(most, tiles ? units : 1);
     }
     if (g.a.requests > 1) {
-        total = wave_sum(total);
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1)
-            most = max(most, __shfl_xor(most, off, 64));
+        total = wave_all(total, Add());
+        most = (int)wave_all((float)most, Max());  // at most 2^24: exact
     }
     const int least = (most + kMaxChunks - 1) / kMaxChunks;
     int chunk = max((int)fminf(__builtin_ceilf(total / want), 16777216.0f), least);
-    if (g.a.requests > 1 && g.a.requests <= 64) {
+    if (g.a.requests > 1 && g.a.requests <= 64 && total > want) {
         for (int again = 0; again < 2; ++again) {
-            const float count = wave_sum((float)(tiles * ((units + chunk - 1) / chunk)));
+            const float count = wave_all((float)(tiles * ((units + chunk - 1) / chunk)), Add());
             if (count > want)
                 chunk = max(min((int)fminf(__builtin_ceilf((float)chunk * (count / want)), 16777216.0f), most), chunk);
         }
@@ -380,16 +370,10 @@ __global__ __launch_bounds__(256) void attn_join_few(const AttnArgs g)
         }
         const float2 s0 = lane < chunks ? *few_part(g, D, kh, first + lane * tiles + tile, cr).stats : none;
         const float2 s1 = lane + 64 < chunks ? *few_part(g, D, kh, first + (lane + 64) * tiles + tile, cr).stats : none;
-        float m = fmaxf(s0.x, s1.x);
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1)
-            m = fmaxf(m, __shfl_xor(m, off, 64));
+        float m = wave_all(fmaxf(s0.x, s1.x), Max());
         m = m == kNone ? 0.0f : m;
         const float f0 = __builtin_amdgcn_exp2f(s0.x - m), f1 = __builtin_amdgcn_exp2f(s1.x - m);
-        float l = s0.y * f0 + s1.y * f1;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1)
-            l += __shfl_xor(l, off, 64);
+        const float l = wave_all(s0.y * f0 + s1.y * f1, Add());
         if (threadIdx.x < 64) {
             weight[lane] = f0;
             weight[lane + 64] = f1;

@@ -119,6 +119,44 @@ struct Add {
     __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
 
+// A value of another lane of the same 16 (DPP control CTRL); lanes without one,
+// and rows of 16 that ROWS leaves out, get `none`.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ int dpp(int x, int none)
+{
+    return __builtin_amdgcn_update_dpp(none, x, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_all(float x)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
+
+// The sum (maximum) over a wavefront in every lane, without LDS: rotations by 8,
+// 4, 2 and 1 within 16 lanes, then the rows of 16.
+template <class OP>
+__device__ __forceinline__ float wave_all(float x, OP op)
+{
+    x = op(x, dpp_all<0x128>(x));
+    x = op(x, dpp_all<0x124>(x));
+    x = op(x, dpp_all<0x122>(x));
+    x = op(x, dpp_all<0x121>(x));
+    return across32(across16(x, op), op);
+}
+
+// Inclusive sum over the lanes up to this one: shifts within 16 lanes, then the
+// last lane of each row of 16 to the next rows.
+__device__ __forceinline__ int wave_scan(int x)
+{
+    x += dpp<0x111>(x, 0);
+    x += dpp<0x112>(x, 0);
+    x += dpp<0x114>(x, 0);
+    x += dpp<0x118>(x, 0);
+    x += dpp<0x142, 0xA>(x, 0);
+    x += dpp<0x143, 0xC>(x, 0);
+    return x;
+}
+
 // A 32-bit word that the whole wavefront reads from device memory that the
 // kernel does not write: one scalar load.
 __device__ __forceinline__ int uniform_word(const int32_t *p)
@@ -149,15 +187,7 @@ __device__ __forceinline__ bool find_item(Walk &w, int requests, int item, int &
         int mine = 0, mine2 = 0;
         if (w.base + lane < requests)
             mine = count(w.base + lane, mine2);
-        int upto = mine, upto2 = mine2;
-        if (requests > 1) {
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-                const int x = __shfl_up(upto, off, 64), y = TWO ? __shfl_up(upto2, off, 64) : 0;
-                upto += lane >= off ? x : 0;
-                upto2 += lane >= off ? y : 0;
-            }
-        }
+        const int upto = wave_scan(mine), upto2 = TWO ? wave_scan(mine2) : 0;
         const unsigned long long has = __ballot(item - w.before < upto);
         if (has) {
             const int at = __builtin_ctzll(has);
@@ -166,9 +196,9 @@ __device__ __forceinline__ bool find_item(Walk &w, int requests, int item, int &
             front = TWO ? w.before2 + __builtin_amdgcn_readlane(upto2, at) - __builtin_amdgcn_readlane(mine2, at) : 0;
             return true;
         }
-        w.before += __builtin_amdgcn_readlane(upto, requests > 1 ? 63 : 0);
+        w.before += __builtin_amdgcn_readlane(upto, 63);
         if (TWO)
-            w.before2 += __builtin_amdgcn_readlane(upto2, requests > 1 ? 63 : 0);
+            w.before2 += __builtin_amdgcn_readlane(upto2, 63);
     }
     return false;
 }
