@@ -203,8 +203,9 @@ __global__ __launch_bounds__(256) void adapters_up(const AdapterArgs g)
     const bq_adapters &a = g.a;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, q4 = lane >> 4;
     const int64_t row0 = (int64_t)blockIdx.y * kUpRows + 64 * wave;
-    // four rows at a time where every row of y and out starts at a multiple of 16 bytes
-    const bool wide = (((uintptr_t)a.y | (uintptr_t)a.out | (uintptr_t)(4 * a.ld_y) | (uintptr_t)(4 * a.ld_out)) & 15) == 0;
+    // four rows at a time, at any multiple of 4 bytes; the matrix's last rows one by one
+    typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+    const bool full = row0 + 64 <= a.rows;
     Walk walk;
     int b, first, end;
     for (int item = blockIdx.x; adapter_item<16 * NT>(g, walk, item, b, first, end); item += gridDim.x) {
@@ -225,23 +226,21 @@ __global__ __launch_bounds__(256) void adapters_up(const AdapterArgs g)
         for (int t0 = first; t0 < end; t0 += 16 * NT) {
             f32x4 sum[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+                const int t = min(t0 + 16 * n + c16, end - 1);
+                const float *y = a.y + (int64_t)t * a.ld_y + row0 + 4 * q4;
+                if (full) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = t0 + 16 * n + c16;
-                    const int64_t row = row0 + 16 * r + 4 * q4;
-                    const float *y = a.y + (int64_t)t * a.ld_y + row;
-                    sum[n][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                    if (wide && row + 4 <= a.rows) {
-                        if (t < end)
-                            sum[n][r] = *reinterpret_cast<const f32x4 *>(y);
-                    } else {
+                    for (int r = 0; r < 4; ++r)
+                        sum[n][r] = *reinterpret_cast<const f32x4u *>(y + 16 * r);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (t < end && row + e < a.rows)
-                                sum[n][r][e] = y[e];
-                    }
+                            sum[n][r][e] = row0 + 16 * r + 4 * q4 + e < a.rows ? y[16 * r + e] : 0.0f;
                 }
+            }
             if (has) {
                 // four ranks of a token at a time; the loads of four pieces, for all that a thread has, before their sums
                 constexpr int QUADS = 16 * NT * 8 * KS, MINE = (QUADS + 255) / 256;
@@ -293,22 +292,24 @@ __global__ __launch_bounds__(256) void adapters_up(const AdapterArgs g)
                 __syncthreads();
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+                const int t = t0 + 16 * n + c16;
+                float *out = a.out + (int64_t)t * a.ld_out + row0 + 4 * q4;
+                if (t >= end)
+                    continue;
+                if (full) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = t0 + 16 * n + c16;
-                    const int64_t row = row0 + 16 * r + 4 * q4;
-                    float *out = a.out + (int64_t)t * a.ld_out + row;
-                    if (wide && row + 4 <= a.rows) {
-                        if (t < end)
-                            *reinterpret_cast<f32x4 *>(out) = sum[n][r];
-                    } else {
+                    for (int r = 0; r < 4; ++r)
+                        *reinterpret_cast<f32x4u *>(out + 16 * r) = sum[n][r];
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (t < end && row + e < a.rows)
-                                out[e] = sum[n][r][e];
-                    }
+                            if (row0 + 16 * r + 4 * q4 + e < a.rows)
+                                out[16 * r + e] = sum[n][r][e];
                 }
+            }
         }
     }
 }
