@@ -24,7 +24,7 @@ struct AdapterArgs {
     bq_adapters a;
     int pieces;       // of n
     int piece;        // values of n in each
-    int down_items;   // items along the grid, 16 NT tokens each
+    int down_items;   // items along the grid: of 16 or 32 tokens, and of 16
     int up_items;
     int direct;       // item i is request i (few tokens each), else the items of all requests are counted through
 };
@@ -193,13 +193,15 @@ __global__ __launch_bounds__(256) void adapters_down(const AdapterArgs g)
 }
 
 // out[t][row] = y[t][row] + B[row] . u[t]: 64 rows of B a wavefront, in
-// registers, along the result's rows; 16 NT tokens along its columns.  The
-// pieces of u are added up once for the workgroup's wavefronts, in LDS.
-template <class T, int KS, int NT>
+// registers, along the result's rows; 16 tokens along its columns.  The pieces
+// of u are added up once for the workgroup's wavefronts, in LDS.  (32 tokens an
+// item read B and u half as often, but leave two wavefronts a SIMD where four
+// fit: 19.3 against 17.1 us for 1000 tokens x 4096 rows of rank 64.)
+template <class T, int KS>
 __global__ __launch_bounds__(256) void adapters_up(const AdapterArgs g)
 {
     typedef T t8 __attribute__((ext_vector_type(8)));
-    __shared__ float us[16 * NT][32 * KS + 4];
+    __shared__ float us[16][32 * KS + 4];
     const bq_adapters &a = g.a;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, q4 = lane >> 4;
     const int64_t row0 = (int64_t)blockIdx.y * kUpRows + 64 * wave;
@@ -208,7 +210,7 @@ __global__ __launch_bounds__(256) void adapters_up(const AdapterArgs g)
     const bool full = row0 + 64 <= a.rows;
     Walk walk;
     int b, first, end;
-    for (int item = blockIdx.x; adapter_item<16 * NT>(g, walk, item, b, first, end); item += gridDim.x) {
+    for (int item = blockIdx.x; adapter_item<16>(g, walk, item, b, first, end); item += gridDim.x) {
         const int id = uniform_word(a.ids + b);
         const bool has = (unsigned)id < (unsigned)a.count;
         if (!has && a.y == a.out)
@@ -223,27 +225,25 @@ __global__ __launch_bounds__(256) void adapters_up(const AdapterArgs g)
                               ? *reinterpret_cast<const t8 *>(static_cast<const T *>(a.b) + ((int64_t)id * a.rows + row) * a.rank + 32 * k + 8 * q4)
                               : t8{};
         }
-        for (int t0 = first; t0 < end; t0 += 16 * NT) {
-            f32x4 sum[NT][4];
+        for (int t0 = first; t0 < end; t0 += 16) {
+            const int t = t0 + c16;
+            const float *y = a.y + (int64_t)min(t, end - 1) * a.ld_y + row0 + 4 * q4;
+            float *out = a.out + (int64_t)t * a.ld_out + row0 + 4 * q4;
+            f32x4 sum[4];
+            if (full) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int t = min(t0 + 16 * n + c16, end - 1);
-                const float *y = a.y + (int64_t)t * a.ld_y + row0 + 4 * q4;
-                if (full) {
+                for (int r = 0; r < 4; ++r)
+                    sum[r] = *reinterpret_cast<const f32x4u *>(y + 16 * r);
+            } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        sum[n][r] = *reinterpret_cast<const f32x4u *>(y + 16 * r);
-                } else {
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            sum[n][r][e] = row0 + 16 * r + 4 * q4 + e < a.rows ? y[16 * r + e] : 0.0f;
-                }
+                    for (int e = 0; e < 4; ++e)
+                        sum[r][e] = row0 + 16 * r + 4 * q4 + e < a.rows ? y[16 * r + e] : 0.0f;
             }
             if (has) {
                 // four ranks of a token at a time; the loads of four pieces, for all that a thread has, before their sums
-                constexpr int QUADS = 16 * NT * 8 * KS, MINE = (QUADS + 255) / 256;
+                constexpr int QUADS = 16 * 8 * KS, MINE = (QUADS + 255) / 256;
                 f32x4 u[MINE];
 #pragma unroll
                 for (int i = 0; i < MINE; ++i)
@@ -252,11 +252,11 @@ __global__ __launch_bounds__(256) void adapters_up(const AdapterArgs g)
                     f32x4 x[MINE][4];
 #pragma unroll
                     for (int i = 0; i < MINE; ++i) {
-                        const int q = threadIdx.x + 256 * i, r = q % (8 * KS) * 4, t = t0 + q / (8 * KS);
-                        const float *p = static_cast<const float *>(a.work) + (int64_t)t * a.rank + r;
+                        const int q = threadIdx.x + 256 * i, r = q % (8 * KS) * 4, tok = t0 + q / (8 * KS);
+                        const float *p = static_cast<const float *>(a.work) + (int64_t)tok * a.rank + r;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            x[i][k] = q < QUADS && r < a.rank && t < end && j + k < g.pieces
+                            x[i][k] = q < QUADS && r < a.rank && tok < end && j + k < g.pieces
                                           ? *reinterpret_cast<const f32x4 *>(p + (int64_t)(j + k) * a.tokens * a.rank)
                                           : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                     }
@@ -271,44 +271,34 @@ __global__ __launch_bounds__(256) void adapters_up(const AdapterArgs g)
                         *reinterpret_cast<f32x4 *>(&us[q / (8 * KS)][q % (8 * KS) * 4]) = u[i];
                 }
                 __syncthreads();
+                f32x4 acc[4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    f32x4 acc[4];
+                for (int r = 0; r < 4; ++r)
+                    acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        Step<T, float> s;
-                        s.set(*reinterpret_cast<const typename Step<T, float>::raw *>(&us[16 * n + c16][32 * k + 8 * q4]));
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            acc[r] = s.add(w[r][k], acc[r]);
-                    }
+                for (int k = 0; k < KS; ++k) {
+                    Step<T, float> s;
+                    s.set(*reinterpret_cast<const typename Step<T, float>::raw *>(&us[c16][32 * k + 8 * q4]));
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        sum[n][r] += acc[r];
+                        acc[r] = s.add(w[r][k], acc[r]);
                 }
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    sum[r] += acc[r];
                 __syncthreads();
             }
+            if (t < end && full) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int t = t0 + 16 * n + c16;
-                float *out = a.out + (int64_t)t * a.ld_out + row0 + 4 * q4;
-                if (t >= end)
-                    continue;
-                if (full) {
+                for (int r = 0; r < 4; ++r)
+                    *reinterpret_cast<f32x4u *>(out + 16 * r) = sum[r];
+            } else if (t < end) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        *reinterpret_cast<f32x4u *>(out + 16 * r) = sum[n][r];
-                } else {
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (row0 + 16 * r + 4 * q4 + e < a.rows)
-                                out[16 * r + e] = sum[n][r][e];
-                }
+                    for (int e = 0; e < 4; ++e)
+                        if (row0 + 16 * r + 4 * q4 + e < a.rows)
+                            out[16 * r + e] = sum[r][e];
             }
         }
     }
@@ -325,7 +315,7 @@ static AdapterArgs adapters_plan(const bq_adapters &a)
         const int64_t all = a.tokens / tokens + a.requests, each = (most + tokens - 1) / tokens * a.requests;
         return g.direct ? (int64_t)a.requests : all < each ? all : each;
     };
-    const int64_t down = items(g.direct ? 16 : 32), up = items(g.direct ? 16 : 32);
+    const int64_t down = items(g.direct ? 16 : 32), up = items(16);
     // pieces of n until a workgroup a compute unit runs, none of fewer than 512 values
     int64_t pieces = 256 / down, cap = a.n / 512;
     pieces = pieces > cap ? cap : pieces;
@@ -359,20 +349,17 @@ static void down_rank(const AdapterArgs &g, hipStream_t st)
 }
 
 template <class T, int KS>
-static void up_nt(const AdapterArgs &g, hipStream_t st)
+static void up_rank(const AdapterArgs &g, hipStream_t st)
 {
     const dim3 grid((unsigned)g.up_items, (unsigned)((g.a.rows + kUpRows - 1) / kUpRows));
-    if (g.direct)
-        hipLaunchKernelGGL((adapters_up<T, KS, 1>), grid, dim3(256), 0, st, g);
-    else
-        hipLaunchKernelGGL((adapters_up<T, KS, 2>), grid, dim3(256), 0, st, g);
+    hipLaunchKernelGGL((adapters_up<T, KS>), grid, dim3(256), 0, st, g);
 }
 
 template <class T>
 static void adapters_type(const AdapterArgs &g, hipStream_t st)
 {
     g.a.x_type == BQ_F32 ? down_rank<T, float>(g, st) : down_rank<T, T>(g, st);
-    g.a.rank <= 32 ? up_nt<T, 1>(g, st) : g.a.rank <= 64 ? up_nt<T, 2>(g, st) : up_nt<T, 4>(g, st);
+    g.a.rank <= 32 ? up_rank<T, 1>(g, st) : g.a.rank <= 64 ? up_rank<T, 2>(g, st) : up_rank<T, 4>(g, st);
 }
 
 hipError_t launch_adapters(const bq_adapters &a, hipStream_t st)
