@@ -111,7 +111,8 @@ template <class T> struct Step<T, float> {
 };
 
 // u[piece][t][r] = gain A[r] . x[t] over a piece of n: ranks along the result's
-// rows (RT tiles of 16), tokens along its columns (NT tiles).
+// rows (RT tiles of 16, a grid row for every 64), tokens along its columns (NT
+// tiles).
 template <class T, class X, int RT, int NT>
 __global__ __launch_bounds__(256) void adapters_down(const AdapterArgs g)
 {
@@ -120,7 +121,7 @@ __global__ __launch_bounds__(256) void adapters_down(const AdapterArgs g)
     __shared__ float red[4][NT][RT][16][17];
     const bq_adapters &a = g.a;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, q4 = lane >> 4;
-    const int piece = blockIdx.x % g.pieces;
+    const int piece = blockIdx.x % g.pieces, rank0 = blockIdx.y * 16 * RT;
     const int64_t from = (int64_t)piece * g.piece, to = min(from + g.piece, a.n);
     Walk walk;
     int b, first, end;
@@ -132,7 +133,7 @@ __global__ __launch_bounds__(256) void adapters_down(const AdapterArgs g)
         const T *w[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
-            w[r] = static_cast<const T *>(a.a) + ((int64_t)id * a.rank + min(16 * r + c16, a.rank - 1)) * a.n + 8 * q4;
+            w[r] = static_cast<const T *>(a.a) + ((int64_t)id * a.rank + min(rank0 + 16 * r + c16, a.rank - 1)) * a.n + 8 * q4;
         for (int t0 = first; t0 < end; t0 += 16 * NT) {
             f32x4 acc[NT][RT];
             const X *x[NT];
@@ -179,12 +180,12 @@ __global__ __launch_bounds__(256) void adapters_down(const AdapterArgs g)
             __syncthreads();
             for (int u = threadIdx.x; u < NT * 16 * RT * 16; u += 256) {
                 const int r = u % (16 * RT), t = u / (16 * RT);
-                if (r < a.rank && t0 + t < end) {
+                if (rank0 + r < a.rank && t0 + t < end) {
                     float sum = 0.0f;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         sum += red[k][t >> 4][r >> 4][t & 15][r & 15];
-                    static_cast<float *>(a.work)[((int64_t)piece * a.tokens + t0 + t) * a.rank + r] = sum * gain;
+                    static_cast<float *>(a.work)[((int64_t)piece * a.tokens + t0 + t) * a.rank + rank0 + r] = sum * gain;
                 }
             }
             __syncthreads();
@@ -333,7 +334,7 @@ int64_t adapters_work(const bq_adapters &a) { return adapters_plan(a).pieces * a
 template <class T, class X, int RT>
 static void down_nt(const AdapterArgs &g, hipStream_t st)
 {
-    const dim3 grid((unsigned)(g.down_items * g.pieces));
+    const dim3 grid((unsigned)(g.down_items * g.pieces), (unsigned)((g.a.rank + 16 * RT - 1) / (16 * RT)));
     if (g.direct)
         hipLaunchKernelGGL((adapters_down<T, X, RT, 1>), grid, dim3(256), 0, st, g);
     else
@@ -344,8 +345,7 @@ template <class T, class X>
 static void down_rank(const AdapterArgs &g, hipStream_t st)
 {
     const int rank = g.a.rank;
-    rank <= 16 ? down_nt<T, X, 1>(g, st) : rank <= 32 ? down_nt<T, X, 2>(g, st)
-        : rank <= 64 ? down_nt<T, X, 4>(g, st) : down_nt<T, X, 8>(g, st);
+    rank <= 16 ? down_nt<T, X, 1>(g, st) : rank <= 32 ? down_nt<T, X, 2>(g, st) : down_nt<T, X, 4>(g, st);
 }
 
 template <class T, int KS>
