@@ -503,7 +503,8 @@ int bq_paged_attn_work_bytes(const bq_attn *a, int64_t *bytes);
  * in parts that carry 22 bits or more.
  * cu (requests + 1) and ids are int32 device arrays, gain f32; max_new
  * (host) bounds the rows of any request and only affects how the work is
- * split.  n is a multiple of 8, rank a multiple of 8 up to 128.  x, a, b and
+ * split.  n is a multiple of 8, rank a multiple of 8 up to 128, requests at
+ * most 2^30.  x, a, b and
  * work are 16-byte aligned, ld_x a multiple of 16 bytes; y and out 4-byte.
  * work (bq_adapters_work_bytes bytes) is scratch of this call until it has
  * run: calls that may run at the same time need one each.  tokens = 0 or

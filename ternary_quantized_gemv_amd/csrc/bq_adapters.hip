@@ -324,8 +324,9 @@ static AdapterArgs adapters_plan(const bq_adapters &a)
     const int64_t steps = (a.n + kDownStep - 1) / kDownStep, per = (steps + pieces - 1) / pieces;
     g.piece = (int)(per * kDownStep);
     g.pieces = (int)((steps + per - 1) / per);
-    g.down_items = (int)(down < (1 << 24) ? down : 1 << 24);  // the kernels walk on from there
-    g.up_items = (int)(up < (1 << 24) ? up : 1 << 24);
+    // a grid holds fewer than 2^32 threads along x; the kernels walk on from there
+    g.down_items = (int)(down < (1 << 22) ? down : 1 << 22);
+    g.up_items = (int)(up < (1 << 22) ? up : 1 << 22);
     return g;
 }
 

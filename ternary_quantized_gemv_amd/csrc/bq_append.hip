@@ -7,6 +7,8 @@
 // either way are f32 series.  One workgroup computes them once for all heads
 // of a token.  Memory bounds the prompt form (everything is read and written
 // once), latency the single token.
+#include <type_traits>
+
 #include "bq_half.h"
 #include "bq_layer.h"
 
@@ -188,7 +190,7 @@ static void append_dim(const AppendArgs &g, unsigned blocks, hipStream_t st)
         hipLaunchKernelGGL((append_kernel<T, C, 128>), dim3(blocks), dim3(kAppendThreads), 0, st, g);
 }
 
-hipError_t launch_append(const bq_append &a, hipStream_t st)
+static void append_slice(const bq_append &a, hipStream_t st)
 {
     AppendArgs g;
     g.a = a;
@@ -205,6 +207,27 @@ hipError_t launch_append(const bq_append &a, hipStream_t st)
         append_dim<_Float16, _Float16>(g, blocks, st);
     else
         append_dim<__bf16, __bf16>(g, blocks, st);
+}
+
+hipError_t launch_append(const bq_append &a, hipStream_t st)
+{
+    // a grid holds fewer than 2^32 threads: 2^17 tokens have at most 2^17 + 2^11 * 2048 workgroups
+    const int64_t most = int64_t(1) << 17;
+    auto rows = [](auto *p, int64_t elems, int type) {
+        typedef std::conditional_t<std::is_const_v<std::remove_pointer_t<decltype(p)>>, const char, char> byte;
+        return p ? static_cast<byte *>(p) + elems * (type == BQ_F32 ? 4 : 2) : nullptr;
+    };
+    for (int64_t t = 0; t < a.tokens; t += most) {
+        bq_append s = a;
+        s.tokens = a.tokens - t < most ? a.tokens - t : most;
+        s.q = rows(a.q, t * a.ld_q, a.type);
+        s.k = rows(a.k, t * a.ld_k, a.type);
+        s.v = rows(a.v, t * a.ld_v, a.type);
+        s.q_out = rows(a.q_out, t * a.ld_qo, a.q_out_type);
+        s.pos = a.pos + t;
+        s.slot = a.slot + t;
+        append_slice(s, st);
+    }
     return hipGetLastError();
 }
 

@@ -414,7 +414,7 @@ __global__ __launch_bounds__(256) void attn_join_many(const AttnArgs g)
 {
     const bq_attn &a = g.a;
     constexpr int L = D / 8;
-    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
+    const int64_t row = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x) / L;
     const int d8 = threadIdx.x % L * 8, chunks = g.p.many.chunks;
     if (row >= a.tokens * a.q_heads)
         return;
@@ -543,7 +543,8 @@ static void join_type(const AttnArgs &g, hipStream_t st)
     }
     if (g.p.many.chunks > 1) {
         const int64_t blocks = (a.tokens * a.q_heads * (D / 8) + 255) / 256;
-        hipLaunchKernelGGL((attn_join_many<OT, D>), dim3((unsigned)blocks), dim3(256), 0, st, g);
+        const int64_t x = blocks < (1 << 20) ? blocks : 1 << 20, y = (blocks + x - 1) / x;  // fewer than 2^32 threads along x
+        hipLaunchKernelGGL((attn_join_many<OT, D>), dim3((unsigned)x, (unsigned)y), dim3(256), 0, st, g);
     }
 }
 

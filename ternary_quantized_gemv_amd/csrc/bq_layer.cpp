@@ -120,8 +120,8 @@ int check_adapters(const char *fn, const bq_adapters *a)
         return set_error(BQ_EARG, "%s: rank %d is not a multiple of 8 in [8, 128]", fn, (int)a->rank);
     if (a->count < 1)
         return set_error(BQ_EARG, "%s: count %d below 1", fn, (int)a->count);
-    if (a->requests < 0)
-        return set_error(BQ_EARG, "%s: requests %d below 0", fn, (int)a->requests);
+    if (a->requests < 0 || a->requests > (1 << 30))
+        return set_error(BQ_EARG, "%s: requests %d not in [0, 2^30]", fn, (int)a->requests);
     if (a->n < 8 || a->n % 8 || a->n >= kRowsMax)
         return set_error(BQ_EARG, "%s: n %lld is not a multiple of 8 in [8, 2^31)", fn, (long long)a->n);
     if (a->rows < 1 || a->rows >= (int64_t(1) << 23))
@@ -258,9 +258,6 @@ BQ_EXPORT int bq_kv_append(const bq_append *a, bq_stream s)
     if (!aligned(a->pos, 4) || !aligned(a->slot, 8) || !aligned(a->freq, 4) || !aligned(a->q_norm, 4) ||
         !aligned(a->k_norm, 4))
         return set_error(BQ_EALIGN, "%s: pos, freq and norm weights must be 4-byte aligned, slot 8-byte", fn);
-    // the grid: a workgroup per token and round of heads, and per eight tokens and 256 value columns
-    if (a->tokens * (((int64_t)a->q_heads + a->cache.heads + 15) / 16 + (nk + 255) / 256 + 1) >= kRowsMax)
-        return set_error(BQ_EARG, "%s: tokens %lld times heads too many for one launch", fn, (long long)a->tokens);
     return launched(fn, launch_append(*a, static_cast<hipStream_t>(s)));
 }
 

@@ -15,11 +15,12 @@ struct NormArgs {
     int8_t *q;
     float *d;
     int64_t ld_x, ld_res, ld_h, ld_y, ld_q, ld_d;
+    int64_t row0;  // of a launch
     int32_t n, qa;
     int32_t f16_scale;
     double eps;
 };
-hipError_t launch_norm(int type, const NormArgs &a, int64_t rows, hipStream_t st);
+hipError_t launch_norm(int type, NormArgs a, int64_t rows, hipStream_t st);
 
 hipError_t launch_append(const bq_append &a, hipStream_t st);
 

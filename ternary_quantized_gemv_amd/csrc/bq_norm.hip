@@ -21,7 +21,7 @@ template <class T, int R>
 __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a)
 {
     __shared__ double sums[16];
-    const int64_t row = blockIdx.x;
+    const int64_t row = a.row0 + blockIdx.x;
     const T *x = static_cast<const T *>(a.x) + row * a.ld_x;
     const T *w = static_cast<const T *>(a.w);
     float v[R][8];
@@ -124,12 +124,17 @@ static void norm_type(const NormArgs &a, int64_t rows, hipStream_t st)
     }
 }
 
-hipError_t launch_norm(int type, const NormArgs &a, int64_t rows, hipStream_t st)
+hipError_t launch_norm(int type, NormArgs a, int64_t rows, hipStream_t st)
 {
-    switch (type) {
-    case BQ_F16: norm_type<_Float16>(a, rows, st); break;
-    case BQ_BF16: norm_type<__bf16>(a, rows, st); break;
-    default: norm_type<float>(a, rows, st); break;
+    // a grid holds fewer than 2^32 threads: at most 2^21 rows of up to 1024 a launch
+    const int64_t most = int64_t(1) << 21;
+    for (a.row0 = 0; a.row0 < rows; a.row0 += most) {
+        const int64_t n = rows - a.row0 < most ? rows - a.row0 : most;
+        switch (type) {
+        case BQ_F16: norm_type<_Float16>(a, n, st); break;
+        case BQ_BF16: norm_type<__bf16>(a, n, st); break;
+        default: norm_type<float>(a, n, st); break;
+        }
     }
     return hipGetLastError();
 }

@@ -62,7 +62,7 @@ CASES = [
         ("ld_q", 264)]),
     ("bq_kv_append", append, [
         ("type", L.BQ_F16), ("q_out_type", L.BQ_F16), ("q_heads", -1), ("q_heads", 1025), ("rot", 24), ("rot", 128),
-        ("rot", -16), ("reserved", 1), ("tokens", -1), ("tokens", (1 << 31) - 1), ("q", None), ("k", None), ("v", None),
+        ("rot", -16), ("reserved", 1), ("tokens", -1), ("tokens", 1 << 31), ("q", None), ("k", None), ("v", None),
         ("q_out", None), ("pos", None), ("slot", None), ("freq", None), ("ld_k", 64), ("ld_q", 128), ("ld_v", 1),
         ("ld_qo", 64), ("q_heads", 0)], [
         ("q", P + 4), ("k", P + 8), ("v", P + 4), ("q_out", P + 4), ("pos", P + 2), ("slot", P + 4), ("freq", P + 1),
@@ -76,7 +76,7 @@ CASES = [
         ("q", P + 4), ("out", P + 8), ("cu", P + 2), ("lens", P + 1), ("table", P + 2), ("ld_q", 258)]),
     ("bq_adapters_add", adapters, [
         ("type", L.BQ_F32), ("x_type", L.BQ_BF16), ("rank", 0), ("rank", 12), ("rank", 136), ("count", 0),
-        ("requests", -1), ("reserved", 1), ("n", 0), ("n", 12), ("rows", 0), ("rows", 1 << 23), ("tokens", -1),
+        ("requests", -1), ("requests", (1 << 30) + 1), ("reserved", 1), ("n", 0), ("n", 12), ("rows", 0), ("rows", 1 << 23), ("tokens", -1),
         ("max_new", 0), ("a", None), ("b", None), ("gain", None), ("x", None), ("cu", None), ("ids", None), ("y", None),
         ("out", None), ("ld_x", 128), ("ld_y", 99), ("ld_out", 99), ("ld_out", 104), ("work", None), ("work_bytes", 16)], [
         ("a", P + 8), ("b", P + 2), ("gain", P + 2), ("x", P + 4), ("cu", P + 1), ("ids", P + 2), ("y", P + 1),
