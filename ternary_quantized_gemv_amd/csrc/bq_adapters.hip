@@ -112,7 +112,9 @@ template <class T> struct Step<T, float> {
 
 // u[piece][t][r] = gain A[r] . x[t] over a piece of n: ranks along the result's
 // rows (RT tiles of 16, a grid row for every 64), tokens along its columns (NT
-// tiles).
+// tiles).  The four wavefronts take turns along n and add up in LDS.  Latency
+// bounds the small calls (16 requests of rank 16, n 4096: 4.2 us), x's reading
+// the large (1000 tokens of rank 64: 11 us).
 template <class T, class X, int RT, int NT>
 __global__ __launch_bounds__(256) void adapters_down(const AdapterArgs g)
 {

@@ -22,7 +22,11 @@
 // bits, q scaled by a power of two per row).  f16 weights are scaled by 2^14 in
 // either case, so that small ones stay clear of f16's subnormals.
 //
-// Memory bounds it: 2 D values a key and head, read once.
+// Memory bounds it: 2 D values a key and head, read once.  Measured with 8 key
+// heads of 128: 64 requests of 8192 keys 6.5 TB/s (a streaming read: 7.1); 32
+// bf16 requests of 3 to 8192 keys 53 us and the join 4.7; one token of f32 rows
+// over 8191 keys 13.3 + 4.5, of which the keys are 5: lengths, table, keys and
+// sums come one behind the other.
 #include "bq_attn.h"
 
 namespace bq {

@@ -18,8 +18,11 @@
 // changes no relative error, and the D sums of a column are not rescaled.
 // (f16 weights are scaled by 2^6, which leaves room for that below 2^16.)
 //
-// The matrix cores bound it: 4 D operations per row and key against 4 D / (128
-// NC) bytes of LDS and less of memory.
+// The matrix cores bound it, with the exponentials in turn: 4 D operations per
+// row and key, and a key's 4 D bytes are read from LDS once for 32 rows and from
+// memory once for 128 or 256.  Measured: 512 bf16 tokens, 32 + 8 heads of 128, over
+// 30011 keys 283 us, 884 TFLOP/s (a large matrix product: 1386); a prompt of 16384
+// tokens 935-960.
 #include "bq_attn.h"
 
 namespace bq {
