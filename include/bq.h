@@ -453,9 +453,11 @@ int bq_kv_append(const bq_append *a, bq_stream s);
  * table_cols of them each) are int32 device arrays, so that a captured graph
  * can be replayed with other lengths; max_new and max_keys (host) bound the
  * new tokens and keys of any request, and only affect how the work is split
- * (larger counts are still computed).  What the device arrays say is bounded
- * in the kernel: rows past `tokens`, keys past table_cols * page and pages
- * outside the cache are not read (keys of such a page count as unseen).
+ * (larger counts are still computed).  cu ascends from 0 or more.  What the
+ * device arrays say is bounded in the kernel: rows past `tokens`, keys past
+ * table_cols * page and pages outside the cache are not read (keys of such a
+ * page count as unseen), and a request that starts below 0, at or past
+ * `tokens`, or at or past its end has no rows.
  * Places of keys below L must hold finite values; others may hold anything.
  * work (device, 16-byte aligned, bq_paged_attn_work_bytes bytes -- some tens
  * of megabytes at most, whatever the tokens and keys -- may be NULL if that is
@@ -501,9 +503,10 @@ int bq_paged_attn_work_bytes(const bq_attn *a, int64_t *bytes);
  * bq_q1_0_matvec's y is row c here); out may be y.  x holds x_type: BQ_F32
  * or the adapters' type.  Sums are f32; f32 values enter the matrix products
  * in parts that carry 22 bits or more.
- * cu (requests + 1) and ids are int32 device arrays, gain f32; max_new
- * (host) bounds the rows of any request and only affects how the work is
- * split.  n is a multiple of 8, rank a multiple of 8 up to 128, requests at
+ * cu (requests + 1, ascending from 0 or more) and ids are int32 device
+ * arrays, gain f32; rows past `tokens` are not touched, a request that ends in
+ * front of its start has none; max_new (host) bounds the rows of any request
+ * and only affects how the work is split.  n is a multiple of 8, rank a multiple of 8 up to 128, requests at
  * most 2^30.  x, a, b and work are 16-byte aligned, ld_x a multiple of 16
  * bytes; y and out 4-byte.  work (bq_adapters_work_bytes bytes) is scratch of
  * this call until it has run: calls that may run at the same time need one

@@ -21,7 +21,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("bq_sweep.hip", "bq_cols.hip", "bq_mf
                                             "bq_floor.hip", "bq_norm.hip", "bq_append.hip", "bq_attn.hip", "bq_attn_tiles.hip", "bq_adapters.hip",
                                             "bq_api.cpp", "bq_layer.cpp", "bq_pack.cpp")]
 HEADERS = [os.path.join(CSRC, f) for f in ("bq_layout.h", "bq_types.h", "bq_device.h", "bq_split.h",
-                                            "bq_launch.h", "bq_half.h", "bq_layer.h", "bq_attn.h")] + [os.path.join(ROOT, "include", "bq.h")]
+                                            "bq_launch.h", "bq_half.h", "bq_layer.h", "bq_attn.h", "bq_rows.h")] + [os.path.join(ROOT, "include", "bq.h")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

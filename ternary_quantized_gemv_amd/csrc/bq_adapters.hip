@@ -41,16 +41,13 @@ __device__ __forceinline__ bool adapter_item(const AdapterArgs &g, Walk &w, int 
             return false;
         b = item;
     } else if (!find_item<false>(w, a.requests, item, b, within, front, [&](int i, int &) {
-                   const int lo = a.cu[i], hi = a.cu[i + 1] > a.tokens ? (int)a.tokens : a.cu[i + 1];
-                   return lo < 0 || hi < lo ? 0 : (hi - lo + TOKENS - 1) / TOKENS;
+                   return (rows_between(a.cu[i], a.cu[i + 1], a.tokens).n + TOKENS - 1) / TOKENS;
                })) {
         return false;
     }
-    first = uniform_word(a.cu + b);
-    end = uniform_word(a.cu + b + 1);
-    end = end > a.tokens ? (int)a.tokens : end;
-    if (first < 0)
-        end = first = 0;
+    const Rows rows = rows_between(uniform_word(a.cu + b), uniform_word(a.cu + b + 1), a.tokens);
+    first = rows.first;
+    end = first + rows.n;
     if (!g.direct) {
         first += within * TOKENS;
         end = min(end, first + TOKENS);

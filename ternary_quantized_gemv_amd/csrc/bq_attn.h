@@ -5,6 +5,7 @@
 
 #include "bq_half.h"
 #include "bq_layer.h"
+#include "bq_rows.h"
 
 namespace bq {
 
@@ -39,10 +40,9 @@ struct Request {
 __device__ __forceinline__ Request request_at(const bq_attn &a, int b)
 {
     Request r;
-    const int lo = uniform_word(a.cu + b), hi = uniform_word(a.cu + b + 1);
-    r.row0 = lo < 0 ? 0 : lo;
-    const int end = hi > a.tokens ? (int)a.tokens : hi;
-    r.n = lo < 0 ? 0 : end - lo;  // a request that starts before the rows is none
+    const Rows rows = rows_between(uniform_word(a.cu + b), uniform_word(a.cu + b + 1), a.tokens);
+    r.row0 = rows.first;
+    r.n = rows.n;
     const int64_t most = (int64_t)a.table_cols * a.cache.page;
     const int len = uniform_word(a.lens + b);
     r.keys = len < 0 ? 0 : len > most ? (int)most : len;
@@ -53,8 +53,7 @@ __device__ __forceinline__ Request request_at(const bq_attn &a, int b)
 // kernel's, which `few` says) and keys.
 __device__ __forceinline__ void lane_request(const AttnArgs &g, int b, bool few, int &rows, int &keys)
 {
-    const int lo = g.a.cu[b], hi = g.a.cu[b + 1], len = g.a.lens[b];
-    const int n = lo < 0 ? 0 : (hi > g.a.tokens ? (int)g.a.tokens : hi) - lo;
+    const int len = g.a.lens[b], n = rows_between(g.a.cu[b], g.a.cu[b + 1], g.a.tokens).n;
     const int64_t most = (int64_t)g.a.table_cols * g.a.cache.page;
     rows = n > 0 && has_few(g.p, n * g.group) == few ? n * g.group : 0;
     keys = len < 0 ? 0 : len > most ? (int)most : len;

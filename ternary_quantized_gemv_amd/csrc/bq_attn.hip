@@ -349,13 +349,12 @@ __global__ __launch_bounds__(256) void attn_join_few(const AttnArgs g)
     const int chunk_units = uniform_word(note_units(g)), first = uniform_word(note_piece(g, blockIdx.y));
     const Request rq = request_at(a, blockIdx.y);
     asm volatile("" ::"s"(chunk_units), "s"(first));
-    const int64_t rows64 = (int64_t)rq.n * g.group;
-    if (rq.n <= 0 || !has_few(g.p, (int)rows64) || (int64_t)blockIdx.x >= (int64_t)rq.n * a.q_heads)
+    if (rq.n <= 0 || !has_few(g.p, rq.n * g.group) || (int64_t)blockIdx.x >= (int64_t)rq.n * a.q_heads)
         return;
     const int chunks = (few_units(rq.keys) + chunk_units - 1) / chunk_units;
     if (chunks <= 1)
         return;
-    const int tiles = few_tiles(g, (int)rows64);
+    const int tiles = few_tiles(g, rq.n * g.group);
     const int grp = threadIdx.x / L, d8 = threadIdx.x % L * 8;
     for (int64_t u = blockIdx.x; u < (int64_t)rq.n * a.q_heads; u += gridDim.x) {
         // row i G + g of key head kh: tile and row of the tile; its pieces are `tiles` apart
@@ -426,14 +425,13 @@ __global__ __launch_bounds__(256) void attn_join_many(const AttnArgs g)
     const int b = request_of(a.cu, a.requests, (int)tok);
     if (b < 0)
         return;
-    // as request_at counts them
-    const int lo = a.cu[b], hi = a.cu[b + 1];
-    const int64_t n = lo < 0 ? 0 : (hi > a.tokens ? a.tokens : hi) - lo;
-    if (n <= 0 || has_few(g.p, (int)(n * g.group)))
+    const Rows mine = rows_between(a.cu[b], a.cu[b + 1], a.tokens);
+    const int n = mine.n;
+    if (n <= 0 || has_few(g.p, n * g.group))
         return;
     // the row's tile, counted from the request's last, and its row there; tiles past the scratch are not split
     const int hq = (int)(row - tok * a.q_heads), kh = hq / g.group, cols = g.p.many.cols;
-    const int r = (int)(tok - lo) * g.group + hq - kh * g.group, tiles = ((int)n * g.group + cols - 1) / cols;
+    const int r = (int)(tok - mine.first) * g.group + hq - kh * g.group, tiles = (n * g.group + cols - 1) / cols;
     const int tile = *note_tile(g, b) + tiles - 1 - r / cols;
     if (tile >= g.p.many.tiles)
         return;
