@@ -22,8 +22,8 @@ constexpr int kUpRows = 256;      // rows of B per workgroup
 
 struct AdapterArgs {
     bq_adapters a;
+    int64_t piece;    // values of n in each of the pieces: up to 2^31
     int pieces;       // of n
-    int piece;        // values of n in each
     int down_items;   // items along the grid: of 16 or 32 tokens, and of 16
     int up_items;
     int direct;       // item i is request i (few tokens each), else the items of all requests are counted through
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(256) void adapters_down(const AdapterArgs g)
     const bq_adapters &a = g.a;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, q4 = lane >> 4;
     const int piece = blockIdx.x % g.pieces, rank0 = blockIdx.y * 16 * RT;
-    const int64_t from = (int64_t)piece * g.piece, to = min(from + g.piece, a.n);
+    const int64_t from = piece * g.piece, to = min(from + g.piece, a.n);
     Walk walk;
     int b, first, end;
     for (int item = blockIdx.x / g.pieces; adapter_item<16 * NT>(g, walk, item, b, first, end); item += gridDim.x / g.pieces) {
@@ -321,7 +321,7 @@ static AdapterArgs adapters_plan(const bq_adapters &a)
     pieces = pieces > cap ? cap : pieces;
     pieces = pieces > kMaxPieces ? kMaxPieces : pieces < 1 ? 1 : pieces;
     const int64_t steps = (a.n + kDownStep - 1) / kDownStep, per = (steps + pieces - 1) / pieces;
-    g.piece = (int)(per * kDownStep);
+    g.piece = per * kDownStep;
     g.pieces = (int)((steps + per - 1) / per);
     // a grid holds fewer than 2^32 threads along x; the kernels walk on from there
     g.down_items = (int)(down < (1 << 22) ? down : 1 << 22);
