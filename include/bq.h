@@ -506,12 +506,13 @@ int bq_paged_attn_work_bytes(const bq_attn *a, int64_t *bytes);
  * cu (requests + 1, ascending from 0 or more) and ids are int32 device
  * arrays, gain f32; rows past `tokens` are not touched, a request that ends in
  * front of its start has none; max_new (host) bounds the rows of any request
- * and only affects how the work is split.  n is a multiple of 8, rank a multiple of 8 up to 128, requests at
- * most 2^30.  x, a, b and work are 16-byte aligned, ld_x a multiple of 16
- * bytes; y and out 4-byte.  work (bq_adapters_work_bytes bytes) is scratch of
- * this call until it has run: calls that may run at the same time need one
- * each.  tokens = 0 or requests = 0 does nothing.  Returns BQ_EARG /
- * BQ_EALIGN before any launch, or BQ_EHIP.  Allocates nothing.  Asynchronous on s. */
+ * and only affects how the work is split.  tokens is at most 2^31 - 64, n a
+ * multiple of 8 below 2^31, rank a multiple of 8 up to 128, requests at most
+ * 2^30, rows below 2^23.  x, a, b and work are 16-byte aligned, ld_x a multiple
+ * of 16 bytes; y and out 4-byte.  work (bq_adapters_work_bytes bytes) is scratch
+ * of this call until it has run: calls that may run at the same time need one
+ * each.  tokens = 0 or requests = 0 does nothing.  Returns BQ_EARG / BQ_EALIGN
+ * before any launch, or BQ_EHIP.  Allocates nothing.  Asynchronous on s. */
 typedef struct bq_adapters {
     int32_t type;   /* of a and b: BQ_F16 or BQ_BF16 */
     int32_t x_type; /* BQ_F32 or type */

@@ -14,6 +14,8 @@ namespace {
 constexpr int64_t kRowsMax = int64_t(1) << 31;
 constexpr int64_t kKeysMax = (int64_t(1) << 31) - (1 << 16);
 constexpr int64_t kLdMax = int64_t(1) << 40;
+// the adapters' kernels count rows in 32 bits up to a tile of 32 past the last one
+constexpr int64_t kAdapterTokens = kRowsMax - 64;
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 bool known(int type) { return type == BQ_F32 || type == BQ_F16 || type == BQ_BF16; }
@@ -106,9 +108,8 @@ int check_adapters(const char *fn, const bq_adapters *a)
 {
     if (!a)
         return set_error(BQ_EARG, "%s: null arguments", fn);
-    const int rc = check_tokens(fn, a->tokens);
-    if (rc)
-        return rc;
+    if (a->tokens < 0 || a->tokens > kAdapterTokens)
+        return set_error(BQ_EARG, "%s: tokens %lld not in [0, 2^31 - 64]", fn, (long long)a->tokens);
     if (a->reserved != 0)
         return set_error(BQ_EARG, "%s: reserved must be 0", fn);
     if (a->type != BQ_F16 && a->type != BQ_BF16)
