@@ -211,9 +211,9 @@ class StagedAttention:
     request is a decode step, whole prompts and chunks of them run the same
     way (the products take up to 16 tokens, the columns of a call, at a time).
 
-    All buffers hold max_tokens rows and are allocated here, so that run()
-    allocates nothing and can be captured into a graph; run() of two blocks on
-    two streams need two objects."""
+    All buffers hold max_tokens rows and are allocated here, on the cache's
+    device, so that run() allocates nothing and can be captured into a graph;
+    run() of two blocks on two streams need two objects."""
 
     COLUMNS = 16  # activation columns of one product call
 
@@ -221,21 +221,23 @@ class StagedAttention:
                  q_norm=None, k_norm=None, adapters=None, eps: float = 1e-6):
         """canon: {"q", "k", "v", "o"} canonical matrices ([q_heads * dim or
         heads * dim, hidden] and [hidden, q_heads * dim]); cache: KVCache;
-        norm: float32 [hidden]; adapters: {"q" / "k" / "v" / "o": Adapters}."""
+        norm: float32 [hidden]; adapters: {"q" / "k" / "v" / "o": Adapters}.
+        All tensors are on the cache's device."""
         import torch
 
+        self.device = cache.k.device
         self.fmt, self.hidden, self.q_heads, self.cache, self.qa, self.eps = fmt, hidden, q_heads, cache, qa, eps
         nq, nk = q_heads * cache.dim, cache.heads * cache.dim
         self.weights = {}
         for name, rows, cols in (("q", nq, hidden), ("k", nk, hidden), ("v", nk, hidden), ("o", hidden, nq)):
             if cols % qa or cols % BLOCK_LEN[fmt]:
                 raise ValueError("every cols must be a multiple of qa and of the block length")
-            self.weights[name] = Weights.upload(fmt, canon[name], rows, cols)
+            self.weights[name] = Weights.upload(fmt, canon[name], rows, cols, device=self.device)
         self.norm, self.freq, self.q_norm, self.k_norm = norm, freq, q_norm, k_norm
         self.adapters = adapters or {}
 
         def rows(n, dtype=torch.float32):
-            return torch.empty(max_tokens, n, dtype=dtype, device="cuda")
+            return torch.empty(max_tokens, n, dtype=dtype, device=self.device)
 
         self.h, self.normed = rows(hidden), rows(hidden)
         self.act, self.act_d = rows(hidden, torch.int8), rows(hidden // qa)
@@ -256,6 +258,12 @@ class StagedAttention:
         bq_adapters_add.  Returns (out, h): this block's output and the
         residual stream that it is to be added to.  With work and adapter_work
         given, nothing is allocated."""
+        import torch
+
+        with torch.cuda.device(self.device):  # whose stream the products take
+            return self._run(x, res, pos, slot, cu, lens, table, max_new, max_keys, ids, work, adapter_work, stream)
+
+    def _run(self, x, res, pos, slot, cu, lens, table, max_new, max_keys, ids, work, adapter_work, stream):
         T = x.shape[0]
         cache, dim = self.cache, self.cache.dim
         q, k, v, o, h, out = (b[:T] for b in (self.q, self.k, self.v, self.o, self.h, self.out))
