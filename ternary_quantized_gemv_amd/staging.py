@@ -213,7 +213,9 @@ class StagedAttention:
 
     All buffers hold max_tokens rows and are allocated here, on the cache's
     device, so that run() allocates nothing and can be captured into a graph;
-    run() of two blocks on two streams need two objects."""
+    run() of two blocks on two streams need two objects.  In a padded batch
+    (rows behind the last request, slot -1) the padding's rows of the output
+    are finite where its rows of x are, and mean nothing."""
 
     COLUMNS = 16  # activation columns of one product call
 
@@ -242,6 +244,8 @@ class StagedAttention:
         self.h, self.normed = rows(hidden), rows(hidden)
         self.act, self.act_d = rows(hidden, torch.int8), rows(hidden // qa)
         self.q, self.k, self.v, self.o = rows(nq), rows(nk), rows(nk), rows(nq)
+        # the attention leaves rows behind the last request as they were, and the quantizer takes finite values
+        self.o.zero_()
         self.o_act, self.o_d, self.out = rows(nq, torch.int8), rows(nq // qa), rows(hidden)
 
     def _product(self, name: str, act, d, y, tokens: int, stream):
