@@ -459,6 +459,8 @@ int bq_kv_append(const bq_append *a, bq_stream s);
  * page count as unseen), and a request that starts below 0, at or past
  * `tokens`, or at or past its end has no rows.
  * Places of keys below L must hold finite values; others may hold anything.
+ * q is finite: the result of a row and head whose query is not has no defined
+ * value; the others' are not touched by it.
  * work (device, 16-byte aligned, bq_paged_attn_work_bytes bytes -- some tens
  * of megabytes at most, whatever the tokens and keys -- may be NULL if that is
  * 0) is scratch of this call until it has run: calls that may run at the same
@@ -502,7 +504,9 @@ int bq_paged_attn_work_bytes(const bq_attn *a, int64_t *bytes);
  * y and out are f32, as the products write them (column c of
  * bq_q1_0_matvec's y is row c here); out may be y.  x holds x_type: BQ_F32
  * or the adapters' type.  Sums are f32; f32 values enter the matrix products
- * in parts that carry 22 bits or more.
+ * in parts that carry 22 bits or more.  x, A and B are finite, and so are A x
+ * and the results: a row of x that is not, or whose A x is not, has NaN where
+ * the formula may have an infinity; the other rows are not touched by it.
  * cu (requests + 1, ascending from 0 or more) and ids are int32 device
  * arrays, gain f32; rows past `tokens` are not touched, a request that ends in
  * front of its start has none; max_new (host) bounds the rows of any request
