@@ -1,7 +1,8 @@
 """bq_rmsnorm_q8 against its definition: quants, scales and the stored sum bit
-for bit (the oracle's quantizer on the normed rows), the normed rows within the
-roundings of their f32 steps; every type, block length, scale flavour, with and
-without residual, in place, strided, one row to many, 32 to 65536 values."""
+for bit (max|v| * fl(1/127) and v / d step by step; f16-valued scales by the
+oracle's narrowing), the normed rows within the roundings of their f32 steps;
+every type, block length, scale flavour, with and without residual, in place,
+strided, one row to many, 32 to 65536 values."""
 import pytest
 
 from gpu_util import bqmod, torch

@@ -58,3 +58,36 @@ def test_f16_scale_of_a_million_blocks(type):
     assert (once != twice).sum() >= 10
     q, d = run(x, w, 32)
     assert t.equal(d, rd) and t.equal(q, rq)
+
+
+@pytest.mark.parametrize("f16_scale", [False, True])
+@pytest.mark.parametrize("qa", [32, 128])
+def test_beside_the_oracles_quantizer(qa, f16_scale):
+    """The norm's scale is max * fl(1/127), the quantizer's amax / 127 (the
+    oracle's, bq_quantize_act_q8's).  fl(1/127) is within 2^-28 of 1/127, so the
+    two f32 scales are at most one unit in the last place apart, and v / d moves
+    by at most 127 (2^-23 + 2 * 2^-24) < 2^-15: the quants are the same but next
+    to half-integers.  Scales as f16 are the same or neighbours."""
+    import oracle
+    t, bq = torch(), bqmod()
+    x, w = normal(gen(3), 300, 4096), normal(gen(4), 4096, scale=0.1, shift=1.0)
+    q, y = t.empty(300, 4096, dtype=t.int8, device="cuda"), t.empty(300, 4096, device="cuda")
+    d = t.empty(300, 4096 // qa, device="cuda")
+    bq.bq_rmsnorm_q8(x.cuda(), w.cuda(), 1e-6, qa, q, d, y=y, f16_scale=f16_scale)
+    v = y.cpu().numpy().reshape(-1, qa)
+    oq, od, _ = oracle.quantize_q8(v.ravel(), qa, f16_scale)
+    got, oq, d = q.cpu().numpy().reshape(-1, qa).astype(int), oq.reshape(-1, qa).astype(int), d.cpu().numpy().ravel()
+    if f16_scale:
+        steps = np.abs(d.astype(np.float16).view(np.int16).astype(int) - od.astype(np.float16).view(np.int16))
+        assert (d == d.astype(np.float16)).all()
+    else:
+        steps = np.abs(d.view(np.int32).astype(np.int64) - od.view(np.int32))
+    assert steps.max() <= 1
+    same = steps == 0
+    assert (got[same] == oq[same]).all()
+    if f16_scale:
+        assert same.mean() > 0.99
+    else:
+        ratio = np.abs(v.astype(np.float64) / od[:, None])
+        border = np.abs(ratio - np.floor(ratio) - 0.5) <= 2.0 ** -15
+        assert (np.abs(got - oq) <= border).all()
