@@ -22,11 +22,18 @@
 // bits, q scaled by a power of two per row).  f16 weights are scaled by 2^14 in
 // either case, so that small ones stay clear of f16's subnormals.
 //
+// 16-bit rows: the weights are rounded to that type once, l sums them in f32
+// before.  Each is off by half a step of the type at most, as out is by its own
+// rounding, and over many keys they average out: relative to the formula in 64
+// bits, in the mean square, bf16 decode rows 1.8e-3 and chunks 2.3e-3, of which
+// out's rounding alone is 1.7e-3.  Two parts would double the second product.
+//
 // Memory bounds it: 2 D values a key and head, read once.  Measured with 8 key
-// heads of 128: 64 requests of 8192 keys 6.5 TB/s (a streaming read: 7.1); 32
-// bf16 requests of 3 to 8192 keys 53 us and the join 4.7; one token of f32 rows
-// over 8191 keys 13.3 + 4.5, of which the keys are 5: lengths, table, keys and
-// sums come one behind the other.
+// heads of 128: 64 requests of 8192 keys 329 us a call, 6.5 TB/s (a streaming
+// read: 7.1); 32 bf16 requests of 3 to 8192 keys 52 us and the join 4.9; 16 bf16
+// tokens over 16384 keys 22 + 5.2; one token of f32 rows over 8191 keys 12.5 +
+// 4.5, of which the keys are 5: lengths, table, keys and sums come one behind
+// the other.
 #include "bq_attn.h"
 
 namespace bq {
@@ -525,8 +532,9 @@ static void attn_nt(const AttnArgs &g, dim3 grid, hipStream_t st)
     case 32: hipLaunchKernelGGL((attn_kernel<CT, D, 1, 2, 4, F32>), grid, dim3(256), 0, st, g); break;
     default:
         // three parts of 128 values for 32 columns a wavefront do not fit its registers: 16 columns, the keys
-        // shared by twice as many (16 tokens over 16384 keys 39.7 -> 37.4 us, 32 x 2048 123 -> 117; two
-        // parts fit and are faster so, 31.6 against 38.7 and 85 against 120)
+        // shared by twice as many (16 tokens over 16384 keys 39.7 -> 37.4 us, 32 x 2048 123 -> 117).  Two parts
+        // need all 256 and 3 more, which are spilled, and are faster so all the same (31.6 against 38.7 and 85
+        // against 120)
         if constexpr (F32 && CT == BQ_BF16 && D == 128)
             hipLaunchKernelGGL((attn_kernel<CT, D, 1, 4, 8, F32>), grid, dim3(512), 0, st, g);
         else
