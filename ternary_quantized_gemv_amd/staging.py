@@ -12,9 +12,13 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (Act, BQ_Q1_0, GroupCall, Weights, bq_adapters_add, bq_kv_append, bq_paged_attn, bq_q1_0_matvec, bq_q2_0_matvec,
-               bq_quantize_act_q8, bq_quantize_act_q8_f16, bq_rmsnorm_q8, bq_sweep_create, bq_sweep_create_x, bq_token_sweep,
-               BLOCK_LEN)
+from . import (Act, BQ_Q1_0, GroupCall, Weights, bq_q1_0_matvec, bq_q2_0_matvec, bq_quantize_act_q8,
+               bq_quantize_act_q8_f16, bq_sweep_create, bq_sweep_create_x, bq_token_sweep, BLOCK_LEN)
+
+try:
+    from . import bq_adapters_add, bq_kv_append, bq_paged_attn, bq_rmsnorm_q8
+except ImportError:  # no torch: what lists the products works without it
+    pass
 
 
 class StagedSweep:
