@@ -545,6 +545,176 @@ typedef struct bq_adapters {
 int bq_adapters_add(const bq_adapters *a, bq_stream s);
 int bq_adapters_work_bytes(const bq_adapters *a, int64_t *bytes);
 
+/* ------------------------------------------------------------------------
+ * Around the layers: what a step of generation runs besides the products of
+ * 1 to 16 columns and the operators above -- the rows of its tokens, the
+ * products of a prompt, the gated activation, the next token.  The
+ * conventions of the section above hold. */
+
+/* Activation functions, evaluated on x:
+ *   BQ_NONE   x
+ *   BQ_SILU   x / (1 + exp(-x))
+ *   BQ_GELU   x / (1 + exp(-2 z)), z = sqrt(2 / pi) (x + 0.044715 x^3), which is
+ *             x (1 + tanh(z)) / 2
+ *   BQ_RELU2  max(x, 0)^2 */
+#define BQ_NONE 0
+#define BQ_SILU 1
+#define BQ_GELU 2
+#define BQ_RELU2 3
+
+/* Rows of a token table, scaled: out[t] = scale * table[ids[t]], each product
+ * rounded once to f32 (a packed weight times its block scale is exact) and
+ * then to `type`.  The table has w.rows rows of w.cols values: packed as the
+ * products' weights (w.fmt BQ_Q1_0 or BQ_Q2_0; the LM head's planes serve
+ * both), or, with w.fmt 0, dense values of dense_type, rows ld_dense elements
+ * apart (w.bits, w.scales NULL; dense NULL where w.fmt is not 0).  A token
+ * whose id is not in [0, w.rows) (-1: padding) gets a row of zeros.  ids is
+ * an int64 device array.  Dense rows and rows of out are 16-byte aligned
+ * (leading dimensions multiples of 16 bytes), w.cols a multiple of 8, and of
+ * the block length where the table is packed, below 2^31.  scale is finite.
+ * out must not overlap the table or ids.  tokens = 0 does nothing.  Returns
+ * BQ_EARG / BQ_EALIGN before any launch, or BQ_EHIP.  Allocates nothing.
+ * Asynchronous on s. */
+typedef struct bq_table {
+    bq_weights w;
+    const void *dense;
+    int64_t ld_dense;
+    int32_t dense_type;
+    int32_t type; /* of out */
+    float scale;
+    int32_t reserved;
+    int64_t tokens;
+    const int64_t *ids;
+    void *out;
+    int64_t ld_out;
+} bq_table;
+int bq_embed(const bq_table *a, bq_stream s);
+
+/* Activation, gate and activation quantizer in one pass: for each of `tokens`
+ * rows of n values,
+ *   v = act(gate) * up, evaluated in binary64 and rounded once to f32
+ *   d, q as bq_rmsnorm_q8 forms them from v (blocks of qa, f16_scale)
+ *   y = v rounded to `type`
+ * so q and d do not hang on how exp is computed (but for a v within 2^-50 of
+ * where it rounds the other way).  gate, up and y hold `type`, rows ld_*
+ * elements apart; y may be NULL, gate or up (same leading dimension), and not
+ * otherwise overlap them.  n is a multiple of qa below 2^31, qa 32, 64 or
+ * 128.  gate, up and y rows are 16-byte aligned, q 8-byte with ld_q a
+ * multiple of 16, d 4-byte.  Values are finite, act(gate) * up too.
+ * tokens = 0 does nothing.  Returns BQ_EARG / BQ_EALIGN before any launch, or
+ * BQ_EHIP.  Allocates nothing.  Asynchronous on s. */
+typedef struct bq_gated {
+    int32_t type;
+    int32_t act; /* BQ_NONE .. BQ_RELU2 */
+    int32_t qa;
+    int32_t f16_scale; /* 0 or 1 */
+    int64_t tokens;
+    int64_t n;
+    const void *gate;
+    int64_t ld_gate;
+    const void *up;
+    int64_t ld_up;
+    int8_t *q;
+    int64_t ld_q;
+    float *d;
+    int64_t ld_d;
+    void *y;
+    int64_t ld_y;
+} bq_gated;
+int bq_gated_q8(const bq_gated *a, bq_stream s);
+
+/* A packed matrix times the quantized activations of any number of tokens:
+ *   y[t, r] = act(sum_k W[r, k] x[t, k] + bias[r]) * mul[t, r] + res[t, r]
+ * with x[t, k] = q[t, k] d[t, k / qa] as the quantizers write it (a.ncols
+ * tokens, 1 to 2^31 - 2^16 of them).  For every block of weights and its
+ * activation scale the sum of w * q is an exact integer; each is scaled by d0
+ * (rounded to f32) and added with d1 by one fma, in f32, in no promised order
+ * over the blocks: the numbers of bq_q1_0_matvec / bq_q2_0_matvec to f32
+ * sums, not their bits.  (A quant of -128, which no quantizer writes, times
+ * -1 gives +128 here.)  Epilogue in f32: bias (f32, w.rows of them), act, mul
+ * and res (both of `type`, as y), each where it is not NULL / BQ_NONE; y is
+ * rounded once.  y may be mul or res (same leading dimension), and not
+ * otherwise overlap an input.  Scales and results are finite.
+ * a.q, w's planes and work are 16-byte aligned (a.ld_q a multiple of 16); the
+ * other arrays by their elements, with any leading dimension of at least
+ * w.rows.  w.cols is below 2^31.
+ * work (bq_matmul_work_bytes bytes; may be NULL if that is 0) is scratch of
+ * this call until it has run: calls that may run at the same time need one
+ * each.  a.ncols = 0 does nothing.  Returns BQ_EARG / BQ_EALIGN before any
+ * launch, or BQ_EHIP.  Allocates nothing.  Asynchronous on s. */
+typedef struct bq_product {
+    bq_weights w;
+    bq_act a;
+    int32_t type; /* of y, mul and res */
+    int32_t act;
+    const float *bias;
+    const void *mul;
+    int64_t ld_mul;
+    const void *res;
+    int64_t ld_res;
+    void *y;
+    int64_t ld_y;
+    void *work;
+    int64_t work_bytes;
+} bq_product;
+int bq_matmul(const bq_product *a, bq_stream s);
+
+/* Bytes of `work` that bq_matmul needs for this argument block (its pointers
+ * are not read).  Host only. */
+int bq_matmul_work_bytes(const bq_product *a, int64_t *bytes);
+
+/* The next token of each of `rows` rows of vocab logits.  With m the row's
+ * largest logit and T its temperature, token i weighs exp((logit[i] - m) / T);
+ * the tokens stand in descending order of their logits, equal ones by index.
+ * Kept are the first of that order, as many as the shortest of these:
+ *   top_k  the first top_k                    (top_k <= 0: all)
+ *   top_p  the fewest whose weights add up to at least top_p times the weight
+ *          of those that top_k keeps          (top_p >= 1: all)
+ *   min_p  those that weigh at least min_p, the largest weight being 1
+ *                                             (min_p <= 0: all)
+ * but at least one.  token is the first of the kept ones at which the running
+ * sum of the weights passes u times their sum (u in [0, 1); others are taken
+ * as the nearer end), logprob the logarithm of its weight over that of all
+ * tokens before the filters.  temperature <= 0 (or NaN) takes the first of the
+ * largest logits, with logprob 0.
+ * Weights are evaluated in binary64 and rounded to multiples of 2^-b (b =
+ * 62 minus the bits of vocab, 39 at least, at most 50), and added up exactly: the
+ * result is the same on any split of the work.
+ * A logit that is NaN or -infinity has no weight; with +infinities only those
+ * weigh.  A row without weight gives token -1 and logprob -infinity.
+ * logits hold `type`, rows ld_logits elements apart (any, at least vocab);
+ * vocab is 1 to 2^22.  u, temperature, top_p, min_p (f32) and top_k (int32)
+ * are device arrays of `rows`; all but u may be NULL (temperature 1, no
+ * filter).  token is an int64, logprob an f32 device array (may be NULL).
+ * Arrays are aligned by their elements, work 16-byte.
+ * work (bq_sample_work_bytes bytes; may be NULL if that is 0) is scratch of
+ * this call until it has run: calls that may run at the same time need one
+ * each.  rows = 0 does nothing.  Returns BQ_EARG / BQ_EALIGN before any
+ * launch, or BQ_EHIP.  Allocates nothing.  Asynchronous on s. */
+#define BQ_VOCAB_MAX (1 << 22)
+typedef struct bq_draw {
+    int32_t type;
+    int32_t reserved;
+    int64_t rows;
+    int64_t vocab;
+    const void *logits;
+    int64_t ld_logits;
+    const float *u;
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+    int64_t *token;
+    float *logprob;
+    void *work;
+    int64_t work_bytes;
+} bq_draw;
+int bq_sample(const bq_draw *a, bq_stream s);
+
+/* Bytes of `work` that bq_sample needs for this argument block (its pointers
+ * are not read).  Host only. */
+int bq_sample_work_bytes(const bq_draw *a, int64_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

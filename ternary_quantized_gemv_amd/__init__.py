@@ -34,6 +34,7 @@ EXPORTS = (
     "bq_token_sweep_noalloc", "bq_set_batch_path",
     "bq_rmsnorm_q8", "bq_kv_append", "bq_paged_attn", "bq_paged_attn_work_bytes", "bq_adapters_add",
     "bq_adapters_work_bytes",
+    "bq_embed", "bq_gated_q8", "bq_matmul", "bq_matmul_work_bytes", "bq_sample", "bq_sample_work_bytes",
 )
 
 
@@ -411,7 +412,7 @@ def bq_token_sweep_noalloc(entries, stream=None) -> None:
     _check(lib.bq_token_sweep_noalloc(arr, len(entries), _stream(stream)))
 
 
-# ------------------------------------- operators between the products (layer.py)
+# --- operators between the products (layer.py) and around the layers (model.py)
 try:
     import torch as _torch  # noqa: F401
 except ImportError:  # as in _load: the host calls work without it
@@ -419,3 +420,5 @@ except ImportError:  # as in _load: the host calls work without it
 else:
     from .layer import (BQ_BF16, BQ_F16, BQ_F32, BQ_NORM_MAX, Adapters, KVCache, bq_adapters_add,  # noqa: F401
                         bq_adapters_work_bytes, bq_kv_append, bq_paged_attn, bq_paged_attn_work_bytes, bq_rmsnorm_q8)
+    from .model import (BQ_GELU, BQ_NONE, BQ_RELU2, BQ_SILU, BQ_VOCAB_MAX, bq_embed, bq_gated_q8, bq_matmul,  # noqa: F401
+                        bq_matmul_work_bytes, bq_sample, bq_sample_work_bytes)

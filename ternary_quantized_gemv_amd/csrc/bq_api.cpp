@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "../../include/bq.h"
+#include "bq_check.h"
 #include "bq_layout.h"
 #include "bq_launch.h"
 #include "bq_types.h"
@@ -108,7 +109,6 @@ static int mfma_choice(int fmt, int tiles, int ncols)
 }
 
 // ------------------------------------------------------------ validation
-static bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 static int hip_check(const char *fn, hipError_t e)
 {
@@ -117,7 +117,7 @@ static int hip_check(const char *fn, hipError_t e)
     return BQ_OK;
 }
 
-static int check_weights(const char *fn, const bq_weights *w, int fmt)
+int check_weights(const char *fn, const bq_weights *w, int fmt)
 {
     if (!w)
         return set_error(BQ_EARG, "%s: null weights", fn);
@@ -140,7 +140,7 @@ static int check_weights(const char *fn, const bq_weights *w, int fmt)
     return BQ_OK;
 }
 
-static int check_act(const char *fn, const bq_act *a, int64_t cols, int max_cols)
+int check_act(const char *fn, const bq_act *a, int64_t cols, int max_cols)
 {
     if (!a)
         return set_error(BQ_EARG, "%s: null activation", fn);

@@ -4,6 +4,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "bq_check.h"
 #include "bq_layer.h"
 #include "bq_layout.h"
 
@@ -11,41 +12,9 @@ using namespace bq;
 
 namespace {
 
-constexpr int64_t kRowsMax = int64_t(1) << 31;
 constexpr int64_t kKeysMax = (int64_t(1) << 31) - (1 << 16);
-constexpr int64_t kLdMax = int64_t(1) << 40;
 // the adapters' kernels count rows in 32 bits up to a tile of 32 past the last one
 constexpr int64_t kAdapterTokens = kRowsMax - 64;
-
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-bool known(int type) { return type == BQ_F32 || type == BQ_F16 || type == BQ_BF16; }
-int size_of(int type) { return type == BQ_F32 ? 4 : 2; }
-
-int launched(const char *fn, hipError_t e)
-{
-    return e == hipSuccess ? BQ_OK : set_error(BQ_EHIP, "%s: %s", fn, hipGetErrorString(e));
-}
-
-// A tensor of `rows` rows of `n` elements of `size` bytes, ld elements apart,
-// each row 16-byte aligned.
-int check_rows(const char *fn, const char *what, const void *p, int64_t ld, int64_t rows, int64_t n, int size)
-{
-    if (!p)
-        return set_error(BQ_EARG, "%s: null %s", fn, what);
-    if (rows > 1 && (ld < n || ld > kLdMax))
-        return set_error(BQ_EARG, "%s: leading dimension %lld of %s below its row length %lld, or above 2^40", fn,
-                         (long long)ld, what, (long long)n);
-    if (!aligned(p, 16) || (rows > 1 && ld * size % 16))
-        return set_error(BQ_EALIGN, "%s: %s rows must be 16-byte aligned", fn, what);
-    return BQ_OK;
-}
-
-int check_tokens(const char *fn, int64_t tokens)
-{
-    if (tokens < 0 || tokens >= kRowsMax)
-        return set_error(BQ_EARG, "%s: tokens %lld not in [0, 2^31)", fn, (long long)tokens);
-    return BQ_OK;
-}
 
 int check_cache(const char *fn, const bq_kv_cache &c)
 {
@@ -129,17 +98,6 @@ int check_adapters(const char *fn, const bq_adapters *a)
         return set_error(BQ_EARG, "%s: rows %lld not in [1, 2^23)", fn, (long long)a->rows);
     if (a->max_new < 1 || a->max_new >= kRowsMax)
         return set_error(BQ_EARG, "%s: max_new %lld not in [1, 2^31)", fn, (long long)a->max_new);
-    return BQ_OK;
-}
-
-int check_work(const char *fn, const void *work, int64_t have, int64_t need)
-{
-    if (need && !work)
-        return set_error(BQ_EARG, "%s: null work", fn);
-    if (have < need)
-        return set_error(BQ_EARG, "%s: work holds %lld bytes, needs %lld", fn, (long long)have, (long long)need);
-    if (need && !aligned(work, 16))
-        return set_error(BQ_EALIGN, "%s: work must be 16-byte aligned", fn);
     return BQ_OK;
 }
 

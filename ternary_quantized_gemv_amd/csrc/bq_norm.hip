@@ -15,6 +15,7 @@
 #include "bq_device.h"
 #include "bq_half.h"
 #include "bq_layer.h"
+#include "bq_quant8.h"
 
 namespace bq {
 
@@ -76,38 +77,10 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a)
             }
         }
         // n and the piece of a wavefront's lanes are multiples of a block: its lanes are all in or all out
-        m = fmaxf(m, __shfl_xor(m, 1, 64));
-        m = fmaxf(m, __shfl_xor(m, 2, 64));
-        if (a.qa > 32)
-            m = fmaxf(m, __shfl_xor(m, 4, 64));
-        if (a.qa > 64)
-            m = fmaxf(m, __shfl_xor(m, 8, 64));
+        m = block_max(m, a.qa);
         if (i >= a.n)
             continue;
-        float db = m * (1.0f / 127.0f), q[8];
-        // the product is rounded to f32 before it is narrowed: seen together, the two become one
-        // instruction that rounds once (another f16 scale for one block in about 2^14)
-        asm("" : "+v"(db));
-        if (a.f16_scale)
-            db = (float)(_Float16)db;
-        if (a.f16_scale && db < 0x1p-14f) {
-            // a subnormal f16 scale is coarser than 1/127 of the maximum: the clamp can bind
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                q[e] = (float)quant_of(v[c][e], db);
-        } else {
-            quant_block<8>(v[c], db, q);
-        }
-        uint32_t lo = 0, hi = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            lo |= (uint32_t)((int)q[e] & 0xFF) << (8 * e);
-            hi |= (uint32_t)((int)q[4 + e] & 0xFF) << (8 * e);
-        }
-        uint2 *qp = reinterpret_cast<uint2 *>(a.q + row * a.ld_q + i);
-        *qp = make_uint2(lo, hi);
-        if (i % a.qa == 0)
-            a.d[row * a.ld_d + i / a.qa] = db;
+        quantize8(v[c], m, a.f16_scale, a.q + row * a.ld_q + i, i % a.qa == 0 ? a.d + row * a.ld_d + i / a.qa : nullptr);
         if (a.y)
             store8(static_cast<T *>(a.y) + row * a.ld_y + i, v[c]);
     }
