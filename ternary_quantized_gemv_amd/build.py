@@ -19,11 +19,11 @@ OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbq.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("bq_sweep.hip", "bq_cols.hip", "bq_mfma.hip", "bq_group.hip", "bq_quantize.hip",
                                             "bq_floor.hip", "bq_norm.hip", "bq_append.hip", "bq_attn.hip", "bq_attn_tiles.hip", "bq_adapters.hip",
-                                            "bq_embed.hip", "bq_gated.hip", "bq_matmul.hip", "bq_sample.hip",
+                                            "bq_embed.hip", "bq_gated.hip", "bq_matmul.hip", "bq_matmul_tiles.hip", "bq_sample.hip",
                                             "bq_api.cpp", "bq_layer.cpp", "bq_model.cpp", "bq_pack.cpp")]
 HEADERS = [os.path.join(CSRC, f) for f in ("bq_layout.h", "bq_types.h", "bq_device.h", "bq_split.h",
                                             "bq_launch.h", "bq_half.h", "bq_layer.h", "bq_attn.h", "bq_rows.h", "bq_check.h", "bq_model.h",
-                                            "bq_quant8.h")] + [os.path.join(ROOT, "include", "bq.h")]
+                                            "bq_quant8.h", "bq_matmul.h")] + [os.path.join(ROOT, "include", "bq.h")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

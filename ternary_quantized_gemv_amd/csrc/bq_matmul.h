@@ -73,95 +73,217 @@ __device__ __forceinline__ void word_q2(const uint32_t (&n)[4], uint32_t (&p)[4]
     p[3] = bytes_of(h23, h01, 0x05040100u);
 }
 
-// The four A operands of a step for token row q (its first quant; valid: values
-// of k that the row has from the step on, a multiple of 32 below 128 at its end).
+// Which words of a row a lane half has.  Where a group is a whole block, half h has
+// words 2 h and 2 h + 1 (8 bytes together); otherwise both halves share the words of
+// a group: words h and 2 + h, or (Q1_0 in groups of 32) half of every word.
+template <int FMT, int QA> struct Words {
+    typedef Shape<FMT, QA> P;
+    static constexpr bool PAIR = P::G == P::BL;
+    static constexpr int N = FMT == BQ_Q1_0 && P::G > 32 ? 2 : 4;  // words a lane and step
+    // first value of k (of the step) that word i of a lane half holds
+    static __device__ __forceinline__ int first(int i, int half)
+    {
+        if constexpr (FMT == BQ_Q1_0)
+            return 32 * (P::G == 32 ? i : PAIR ? 2 * half + i : 2 * i + half);
+        else
+            return 64 * (i / 2) + 16 * (PAIR ? 2 * half + i % 2 : i % 2 * 2 + half);
+    }
+};
+
+// The four A operands of a step for the token row whose quants of the step are at q
+// (the row has `valid` of them, a multiple of 32; the others count as zeros).
 template <int FMT, int QA>
 __device__ __forceinline__ void act_operands(const int8_t *q, int half, int valid, u32x4 (&f)[4])
 {
-    typedef Shape<FMT, QA> P;
-    uint32_t n[4][8];  // the four words of 32 values of the step
+    typedef Words<FMT, QA> W;
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            u32x4 v = {0, 0, 0, 0};
-            if (FMT == BQ_Q1_0 || 32 * w < valid)
-                v = *reinterpret_cast<const u32x4 *>(q + 32 * w + 16 * x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                n[w][4 * x + e] = v[e];
-        }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        uint32_t p[4];
+    for (int i = 0; i < W::N; ++i) {
+        const int k = W::first(i, half);
+        const u32x4 *p = reinterpret_cast<const u32x4 *>(q + k);
         if constexpr (FMT == BQ_Q1_0) {
-            if constexpr (P::G == 32) {  // word m, its halves in the lane halves
-                word_half_q1(n[m], half, p);
-            } else {  // words 2 (m / 2) + half
-                uint32_t mine[8];
+            uint32_t n[8], o[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    mine[e] = half ? n[m / 2 * 2 + 1][e] : n[m / 2 * 2][e];
-                word_half_q1(mine, m & 1, p);
+            for (int x = 0; x < 2; ++x) {
+                const u32x4 v = k < valid ? p[x] : u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    n[4 * x + e] = v[e];
             }
-        } else {  // word 2 (m % 2) + half of block m / 2, 16 quants each
-            uint32_t mine[4];
+            if constexpr (W::N == 4) {
+                word_half_q1(n, half, o);
+                f[i] = u32x4{o[0], o[1], o[2], o[3]};
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                mine[e] = half ? n[m][4 + e] : n[m][e];
-            word_q2(mine, p);
+                for (int x = 0; x < 2; ++x) {
+                    word_half_q1(n, x, o);
+                    f[2 * i + x] = u32x4{o[0], o[1], o[2], o[3]};
+                }
+            }
+        } else {
+            const u32x4 v = k < valid ? *p : u32x4{0, 0, 0, 0};
+            const uint32_t n[4] = {v[0], v[1], v[2], v[3]};
+            uint32_t o[4];
+            word_q2(n, o);
+            f[i] = u32x4{o[0], o[1], o[2], o[3]};
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            f[m][e] = p[e];
     }
 }
 
-// The four B operands of a step from the row's payload words.  Q1_0: w[0], the
-// block's four words; Q2_0: two blocks.
-template <int FMT, int QA>
-__device__ __forceinline__ void weight_operand(const u32x4 (&w)[Shape<FMT, QA>::BLOCKS], int half, int m, i32x4 &f)
+// The packed planes of a tile of 64 rows: uniform bases, 32-bit offsets of the lane's
+// row (no vector addresses are kept).
+struct TileOf {
+    rsrc_t bits, scales;
+};
+template <int FMT>
+__device__ __forceinline__ TileOf tile_of(const bq_weights &w, int64_t tile, int64_t nb)
 {
-    typedef Shape<FMT, QA> P;
+    return TileOf{rsrc_of(static_cast<const u32x4 *>(w.bits) + tile_block0(FMT, tile, nb) * kTileRows),
+                  rsrc_of(reinterpret_cast<const u32x4 *>(w.scales) + tile * ((nb + 7) / 8) * kTileRows)};
+}
+
+// A lane's words of the step that starts with block b, and its scales.  Its row of the
+// tile is row0 (the same in all lanes) + lane % 32; at = 16 (lane % 32) + 8 half.  Past
+// the last block (Q2_0, an odd number of them) the last one again: its quants are zeros.
+template <int FMT, int QA>
+__device__ __forceinline__ void load_weights(const TileOf &t, int row0, int at, int b, int nb, uint32_t (&w)[Words<FMT, QA>::N],
+                                             uint16_t (&d0)[Shape<FMT, QA>::BLOCKS])
+{
+    typedef Words<FMT, QA> W;
+    constexpr int BLOCKS = Shape<FMT, QA>::BLOCKS, EACH = W::N / BLOCKS;
+    const int row = at & ~15, half4 = (at & 8) >> 1;
+#pragma unroll
+    for (int j = 0; j < BLOCKS; ++j) {
+        const uint32_t block = b + j < nb ? b + j : nb - 1, from = block * kStep + row0 * 16;
+        if constexpr (W::PAIR) {
+            const auto v = __builtin_amdgcn_raw_buffer_load_b64(t.bits, at, from, 0);
+            w[2 * j] = v[0];
+            w[2 * j + 1] = v[1];
+        } else if constexpr (W::N == 4 && FMT == BQ_Q1_0) {
+            const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(t.bits, row, from, 0));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = v[i];
+        } else {  // words h and 2 + h
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                w[EACH * j + i] = __builtin_amdgcn_raw_buffer_load_b32(t.bits, row + half4, from + 8 * i, 0);
+        }
+        d0[j] = __builtin_amdgcn_raw_buffer_load_b16(t.scales, row, (block >> 3) * kStep + row0 * 16 + (block & 7) * 2, 0);
+    }
+}
+
+// B operand m of a step from a lane's words.
+template <int FMT, int QA>
+__device__ __forceinline__ i32x4 weight_operand(const uint32_t (&w)[Words<FMT, QA>::N], int half, int m)
+{
+    typedef Words<FMT, QA> W;
+    i32x4 f;
     if constexpr (FMT == BQ_Q1_0) {
-        uint32_t x = P::G == 32 ? w[0][m] : half ? w[0][m / 2 * 2 + 1] : w[0][m / 2 * 2];
-        if constexpr (P::G == 32)
+        uint32_t x = W::N == 4 ? w[m] : w[m / 2];
+        if constexpr (W::N == 4)
             x = half ? x >> 4 | x << 28 : x;
-        const int at = P::G == 32 ? 0 : 4 * (m & 1);
+        const int at = W::N == 4 ? 0 : 4 * (m & 1);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             f[i] = (int32_t)((at + i ? x >> (at + i - 1) : x << 1) & 0x02020202u);
     } else {
-        const uint32_t x = half ? w[m / 2][m % 2 * 2 + 1] : w[m / 2][m % 2 * 2];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            f[i] = (int32_t)(x >> (2 * i) & 0x03030303u);
+            f[i] = (int32_t)(w[m] >> (2 * i) & 0x03030303u);
     }
+    return f;
 }
 
-// The block of the payload plane (in units of 64 rows) where rows r0 .. of a step
-// start, and the row's scale; past the last block (Q2_0, an odd number of them)
-// the last one again: its quants are zeros.
-template <int FMT>
-__device__ __forceinline__ int64_t clamp_block(int64_t b, int64_t nb) { return b < nb ? b : nb - 1; }
-
-// act(x + bias) * mul + res, and the store.
-template <class T>
-__device__ __forceinline__ void finish(const bq_product &a, float x, int64_t t, int64_t r)
+// The sum of a group's quants, from the operands of both lane halves.
+template <int GM>
+__device__ __forceinline__ int quant_sum(const u32x4 *f)
 {
-    if (a.bias)
-        x += a.bias[r];
+    int s = 0;
+#pragma unroll
+    for (int m = 0; m < GM; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            s = __builtin_amdgcn_sdot4((int)f[m][e], 0x01010101, s, false);
+    return s + __shfl_xor(s, 32, 64);
+}
+
+// act(x + bias) * mul + res of row r, and the stores, for tokens t[0 .. N) as far as they
+// are live.  The others' t is the last token: loads of all are under way together.
+template <class T, int N>
+__device__ __forceinline__ void store_rows(const bq_product &a, float (&x)[N], const int64_t (&t)[N], const bool (&live)[N], int64_t r)
+{
+    if (a.mul) {
+        T v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            v[e] = static_cast<const T *>(a.mul)[t[e] * a.ld_mul + r];
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            x[e] *= (float)v[e];
+    }
+    if (a.res) {
+        T v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            v[e] = static_cast<const T *>(a.res)[t[e] * a.ld_res + r];
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            x[e] += (float)v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        if (live[e])
+            static_cast<T *>(a.y)[t[e] * a.ld_y + r] = (T)x[e];
+}
+template <int N>
+__device__ __forceinline__ void finish(const bq_product &a, float (&x)[N], const int64_t (&t)[N], const bool (&live)[N], int64_t r)
+{
+    if (a.bias) {
+        const float b = a.bias[r];
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            x[e] += b;
+    }
     switch (a.act) {
-    case BQ_SILU: x = x / (1.0f + expf(-x)); break;
-    case BQ_GELU: x = x / (1.0f + expf(-1.59576912160573f * __builtin_fmaf(0.044715f * x * x, x, x))); break;
-    case BQ_RELU2: x = fmaxf(x, 0.0f) * fmaxf(x, 0.0f); break;
+    case BQ_SILU:
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            x[e] = x[e] / (1.0f + expf(-x[e]));
+        break;
+    case BQ_GELU:
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            x[e] = x[e] / (1.0f + expf(-1.59576912160573f * __builtin_fmaf(0.044715f * x[e] * x[e], x[e], x[e])));
+        break;
+    case BQ_RELU2:
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            x[e] = fmaxf(x[e], 0.0f) * fmaxf(x[e], 0.0f);
+        break;
     default: break;
     }
-    if (a.mul)
-        x *= (float)static_cast<const T *>(a.mul)[t * a.ld_mul + r];
-    if (a.res)
-        x += (float)static_cast<const T *>(a.res)[t * a.ld_res + r];
-    static_cast<T *>(a.y)[t * a.ld_y + r] = (T)x;
+    switch (a.type) {
+    case BQ_F16: store_rows<_Float16, N>(a, x, t, live, r); break;
+    case BQ_BF16: store_rows<__bf16, N>(a, x, t, live, r); break;
+    default: store_rows<float, N>(a, x, t, live, r); break;
+    }
 }
+
+// Laid-out activations (matmul_lay): for every 128 tokens and step of k a stage of 4 x 4
+// operands (32 tokens and 32 values of k: 64 lanes of 16 bytes), then for every group
+// 128 scales and 128 starting values.
+constexpr int kTileTokens = 128, kTileOut = 256;
+template <int FMT, int QA> struct Stage {
+    static constexpr int QUANTS = kTileTokens * kStepK;
+    static constexpr int BYTES = QUANTS + Shape<FMT, QA>::NG * 1024;
+};
+
+struct MatmulArgs {
+    bq_product p;
+    int64_t token_tiles, row_tiles;  // of the kernel that follows
+    int steps;                       // of k
+};
+// bq_matmul_tiles.hip, behind matmul_lay: 32 or 64 tokens a workgroup
+hipError_t launch_matmul_tiles(MatmulArgs g, int tokens, hipStream_t st);
 
 }  // namespace bq

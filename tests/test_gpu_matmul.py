@@ -50,6 +50,44 @@ def test_products(fmt, qa, T, rows, cols):
     within(y, *matmul_ref(fmt, canon, q, d, qa, DT["f32"]), (fmt, qa, T, rows, cols))
 
 
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("qa", [32, 64, 128])
+@pytest.mark.parametrize("T,rows,cols", [(600, 2000, 128), (601, 2001, 384), (1025, 1030, 640), (2100, 2600, 256), (4100, 1500, 896)])
+def test_many_tokens(fmt, qa, T, rows, cols):
+    """Enough tiles for the kernels of 32 and of 64 tokens a workgroup, ends inside a tile on both sides."""
+    bq = bqmod()
+    canon = synth.blocks(fmt, rows, cols, 7, T)
+    q, d = acts(T, cols, qa, T + rows)
+    y = run(bq.Weights.upload(fmt, canon, rows, cols), q, d, qa, DT["f32"], pad=(T % 2) * 3)
+    within(y, *matmul_ref(fmt, canon, q, d, qa, DT["f32"]), (fmt, qa, T, rows, cols))
+
+
+@pytest.mark.parametrize("qa", [32, 64])
+@pytest.mark.parametrize("T", [600, 2200])
+def test_many_tokens_odd_number_of_blocks(qa, T):
+    bq = bqmod()
+    for cols in (64, 320):
+        canon = synth.q2_0_blocks_all_codes(2500, cols, 3, T)
+        q, d = acts(T, cols, qa, T)
+        y = run(bq.Weights.upload(2, canon, 2500, cols), q, d, qa, DT["f32"])
+        within(y, *matmul_ref(2, canon, q, d, qa, DT["f32"]), (qa, T, cols))
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu2"])
+@pytest.mark.parametrize("T", [601, 2150])
+def test_many_tokens_epilogues(dt, act, T):
+    bq = bqmod()
+    rows, cols, qa, g = 2049, 256, 64, gen(T)
+    canon = synth.blocks(1, rows, cols, 8, T)
+    w = bq.Weights.upload(1, canon, rows, cols)
+    q, d = acts(T, cols, qa, 3)
+    d = d * np.float32(0.3)
+    bias, mul, res = normal(g, rows), normal(g, T, rows, dtype=DT[dt]), normal(g, T, rows, dtype=DT[dt])
+    y = run(w, q, d, qa, DT[dt], bias, act, mul, res, pad=3)
+    within(y, *matmul_ref(1, canon, q, d, qa, DT[dt], bias, act, mul, res), (act, dt))
+
+
 @pytest.mark.parametrize("qa", [32, 64])
 @pytest.mark.parametrize("T", [5, 40, 130, 400])
 @pytest.mark.parametrize("cols", [64, 192, 576, 1088])
@@ -126,22 +164,23 @@ def test_near_the_single_products(fmt):
     _, bound = matmul_ref(fmt, canon, q[:16], d[:16], qa, t.float32)
     y = t.empty(16, rows, device="cuda")
     (bq.bq_q1_0_matvec if fmt == 1 else bq.bq_q2_0_matvec)(w, bq.Act(t.from_numpy(q[:16]).cuda(), t.from_numpy(d[:16]).cuda(), cols, qa, 16), y)
-    for T in (16, 40, 200):
+    q, d = np.tile(q, (20, 1)), np.tile(d, (20, 1))
+    for T in (16, 40, 200, 4000):
         within(run(w, q[:T], d[:T], qa, t.float32)[:16], y.cpu(), 2 * bound, T)
 
 
-@pytest.mark.parametrize("T", [20, 300])
-def test_streams_scratch_and_graphs(T):
+@pytest.mark.parametrize("T,rows", [(20, 300), (300, 300), (610, 2000), (2200, 2500)])
+def test_streams_scratch_and_graphs(T, rows):
     """On another stream, with the caller's scratch, two calls at once, and captured and replayed: the same bits."""
     t, bq = torch(), bqmod()
-    canon = synth.q2_0_blocks(300, 1024, 1)
-    w = bq.Weights.upload(2, canon, 300, 1024)
+    canon = synth.q2_0_blocks(rows, 1024, 1)
+    w = bq.Weights.upload(2, canon, rows, 1024)
     q, d = acts(T, 1024, 64, 6)
     a = bq.Act(t.from_numpy(q).cuda(), t.from_numpy(d).cuda(), 1024, 64, T)
     want = run(w, q, d, 64, t.float32)
     need = bq.bq_matmul_work_bytes(w, T, 64)
     works = [t.empty(need, dtype=t.uint8, device="cuda") for _ in range(2)]
-    ys = [t.zeros(T, 300, device="cuda") for _ in range(2)]
+    ys = [t.zeros(T, rows, device="cuda") for _ in range(2)]
     streams = [t.cuda.Stream() for _ in range(2)]
     t.cuda.synchronize()
     for _ in range(3):
@@ -149,7 +188,7 @@ def test_streams_scratch_and_graphs(T):
             bq.bq_matmul(w, a, y, work=work, stream=s)
     t.cuda.synchronize()
     assert t.equal(ys[0].cpu(), want) and t.equal(ys[1].cpu(), want)
-    y = t.zeros(T, 300, device="cuda")
+    y = t.zeros(T, rows, device="cuda")
     graph = t.cuda.CUDAGraph()
     with t.cuda.graph(graph):
         bq.bq_matmul(w, a, y, work=works[0])
