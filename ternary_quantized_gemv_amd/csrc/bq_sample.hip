@@ -36,51 +36,58 @@ __device__ __forceinline__ float logit_of(uint32_t key)
 
 // What turns a logit into its weight and bucket.
 struct Scale {
-    double top;      // the largest logit
-    double per;      // log2(e) / T
-    float buckets;   // buckets a unit of log2 weight
-    int bits;        // weights are multiples of 2^-bits
+    double top;     // the largest logit
+    double per;     // 32 log2(e) / T
+    float topf;
+    float buckets;  // a unit of logit
+    int bits;       // weights are multiples of 2^-bits
     bool greedy;
 };
 
-// log2 of the weight, at most 0.
-__device__ __forceinline__ double log2_weight(const Scale &s, float l)
+__device__ __forceinline__ Scale scale_of_row(uint32_t top, float t, int vocab)
 {
-    const double x = (double)l - s.top;
-    if ((double)l == s.top)
-        return 0.0;
-    return s.greedy ? -__builtin_inf() : x * s.per;
+    Scale s;
+    s.topf = logit_of(top);
+    s.top = (double)s.topf;
+    s.greedy = !(t > 0.0f);
+    s.per = 32.0 * 1.44269504088896340736 / (double)t;
+    const int wide = 32 - __builtin_clz((unsigned)vocab);
+    s.bits = 62 - wide < 50 ? 62 - wide : 50;
+    // kBuckets of them hold bits + 2 halvings: behind the last one every weight rounds to 0 (bits + 1 would do; f32
+    // is off by far less than that)
+    s.buckets = (float)(kBuckets / 32.0 * s.per / (double)(s.bits + 2));
+    return s;
 }
-// 2^y in units of 2^-bits, rounded to nearest: y = n + f, |f| <= 1/2, 2^f = exp(f ln 2) by
-// its series (the first term left out is below 2^-52 of it); 0 where it is below half a unit.
-__device__ __forceinline__ u64 weight_of(const Scale &s, double y)
+
+// Never falling as the logit falls; kBuckets and more: no weight.  (+infinity minus itself: 0.)
+__device__ __forceinline__ int bucket_of(const Scale &s, float l)
 {
-    if (!(y > -(double)(s.bits + 1)))
+    if (l == s.topf)
         return 0;
-    const double n = __builtin_rint(y), f = (y - n) * 0.69314718055994530942;
-    double p = 1.0 / 479001600.0;
-    p = __builtin_fma(p, f, 1.0 / 39916800.0);
-    p = __builtin_fma(p, f, 1.0 / 3628800.0);
-    p = __builtin_fma(p, f, 1.0 / 362880.0);
-    p = __builtin_fma(p, f, 1.0 / 40320.0);
-    p = __builtin_fma(p, f, 1.0 / 5040.0);
-    p = __builtin_fma(p, f, 1.0 / 720.0);
-    p = __builtin_fma(p, f, 1.0 / 120.0);
+    const float x = (s.topf - l) * s.buckets;
+    return !s.greedy && x < (float)kBuckets ? (int)x : kBuckets;
+}
+// exp((l - top) / T) in units of 2^-bits, before it is rounded: 2^(y / 32) with y = n + f, |f| <= 1/2, of which 2^(f / 32)
+// is exp(f ln 2 / 32) by its series (the first term left out is below 2^-48 of it), and 2^(n % 32 / 32) from a table.
+__device__ __forceinline__ double weight_at(const Scale &s, const double *table, float l)
+{
+    if (l == s.topf)
+        return __builtin_ldexp(1.0, s.bits);
+    const double y = ((double)l - s.top) * s.per, n = __builtin_rint(y), f = (y - n) * (0.69314718055994530942 / 32.0);
+    double p = 1.0 / 120.0;
     p = __builtin_fma(p, f, 1.0 / 24.0);
     p = __builtin_fma(p, f, 1.0 / 6.0);
     p = __builtin_fma(p, f, 0.5);
     p = __builtin_fma(p, f, 1.0);
     p = __builtin_fma(p, f, 1.0);
-    // weights are below 2^52 units: added to 2^52, the low bits hold the rounded number
-    const double w = __builtin_ldexp(p, (int)n + s.bits) + 0x1p52;
-    return __builtin_bit_cast(u64, w) & 0xFFFFFFFFFFFFFull;
+    const int i = (int)n;
+    return __builtin_ldexp(p * table[i & 31], (i >> 5) + s.bits);
 }
-// y > -(bits + 1) - 1/2: never more than kBuckets - 1, and never falling as the logit falls.
-__device__ __forceinline__ int bucket_of(const Scale &s, double y)
-{
-    const int b = (int)((float)-y * s.buckets);
-    return b < kBuckets ? b : kBuckets - 1;
-}
+// Rounded to nearest: below 2^52, so that in the sum with 2^52 the low bits hold the number.
+__device__ __forceinline__ u64 rounded(double w) { return __builtin_bit_cast(u64, w + 0x1p52) & 0xFFFFFFFFFFFFFull; }
+
+// A token's place in the order: larger is earlier.
+__device__ __forceinline__ u64 token_of(float l, int i) { return (u64)key_of(l) << 32 | (uint32_t)~i; }
 
 __device__ __forceinline__ u64 lane_u64(u64 x, int lane)
 {
@@ -95,6 +102,7 @@ struct Room {
     uint32_t count2[kBuckets];  // of parts of one bucket
     u64 mass2[kBuckets];
     u64 list[kList];            // (key, ~index)
+    double table[32];           // 2^(i / 32)
     u64 waves[2][kSampleThreads / 64];
     uint32_t found;
     u64 before_count, before_mass, low, high, answer;
@@ -129,12 +137,40 @@ __device__ __forceinline__ void scan(Room &r, uint32_t &count, u64 &mass)
     __syncthreads();
 }
 
-// The tokens of a row.  Calls f(index, logit) for all of them, each once.
+// Calls f(index, logit) once for each token from lo to hi of a row: 16 bytes a load, four loads under way.
 template <class T, class F>
-__device__ __forceinline__ void each_token(const T *row, int vocab, F f)
+__device__ __forceinline__ void each_token(const T *row, int lo, int hi, F f)
 {
-    for (int i = threadIdx.x; i < vocab; i += kSampleThreads)
-        f(i, (float)row[i]);
+    constexpr int V = 16 / sizeof(T);
+    typedef T vec __attribute__((ext_vector_type(V)));
+    const int tid = threadIdx.x;
+    int head = (int)((16 - ((uintptr_t)(row + lo) & 15)) & 15) / (int)sizeof(T);
+    head = head < hi - lo ? head : hi - lo;
+    if (tid < head)
+        f(lo + tid, (float)row[lo + tid]);
+    const int from = lo + head, n = (hi - from) / V;
+    const vec *p = reinterpret_cast<const vec *>(row + from);
+    int c = tid;
+    for (; c + 3 * kSampleThreads < n; c += 4 * kSampleThreads) {
+        vec v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = p[c + j * kSampleThreads];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                f(from + (c + j * kSampleThreads) * V + e, (float)v[j][e]);
+    }
+    for (; c < n; c += kSampleThreads) {
+        const vec v = p[c];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            f(from + c * V + e, (float)v[e]);
+    }
+    const int rest = from + n * V + tid;
+    if (rest < hi)
+        f(rest, (float)row[rest]);
 }
 
 // A place of the descending order: the sum of weights up to and with its token.
@@ -144,9 +180,10 @@ struct Place {
 };
 
 // The first token at which the running count (by_count) or weight reaches target, which
-// the whole row does (1 <= target).
+// the whole row does (1 <= target).  The tokens of buckets 0 .. known are in the list already
+// (known < 0: none).
 template <class T>
-__device__ Place reach(Room &r, const Scale &s, const T *row, int vocab, bool by_count, u64 target)
+__device__ Place reach(Room &r, const Scale &s, const T *row, int vocab, bool by_count, u64 target, int known)
 {
     const int tid = threadIdx.x;
     {
@@ -162,23 +199,24 @@ __device__ Place reach(Room &r, const Scale &s, const T *row, int vocab, bool by
     u64 n = r.count[bucket] - (uint32_t)r.before_count, before_count = r.before_count, before_mass = r.before_mass;
     // tokens low <= (key, ~index) <= high of the bucket: n of them, the target among them
     u64 low = 0, high = ~0ull;
-    bool from_list = false;
-    int listed = 0;
-    auto member = [&](u64 token) { return token >= low && token <= high; };
+    bool from_list = bucket <= known;
+    int listed = from_list ? (int)r.count[known] : 0;
+    auto weight = [&](u64 token) { return rounded(weight_at(s, r.table, logit_of((uint32_t)(token >> 32)))); };
+    auto member = [&](u64 token) {
+        return token >= low && token <= high && bucket_of(s, logit_of((uint32_t)(token >> 32))) == bucket;
+    };
     auto each = [&](auto f) {
         if (from_list) {
             for (int i = tid; i < listed; i += kSampleThreads)
                 if (member(r.list[i]))
                     f(r.list[i]);
         } else {
-            each_token(row, vocab, [&](int i, float l) {
-                const uint32_t key = key_of(l);
-                const u64 token = (u64)key << 32 | (uint32_t)~i;
-                if (!key || !member(token))
-                    return;
-                const double y = log2_weight(s, l);
-                if (weight_of(s, y) && bucket_of(s, y) == bucket)
-                    f(token);
+            each_token(row, 0, vocab, [&](int i, float l) {
+                if (l > -__builtin_inff() && bucket_of(s, l) == bucket) {
+                    const u64 token = token_of(l, i);
+                    if (token >= low && token <= high)
+                        f(token);
+                }
             });
         }
     };
@@ -227,7 +265,7 @@ __device__ Place reach(Room &r, const Scale &s, const T *row, int vocab, bool by
         each([&](u64 token) {
             const int part = (int)((top - token) >> shift);
             atomicAdd(&r.count2[part], 1u);
-            atomicAdd(&r.mass2[part], weight_of(s, log2_weight(s, logit_of((uint32_t)(token >> 32)))));
+            atomicAdd(&r.mass2[part], weight(token));
         });
         __syncthreads();
         uint32_t c = r.count2[tid];
@@ -259,7 +297,7 @@ __device__ Place reach(Room &r, const Scale &s, const T *row, int vocab, bool by
     if (tid < 64) {
         const bool live = tid < (int)n;
         const u64 token = live ? last[tid] : 0;
-        const u64 w = live ? weight_of(s, log2_weight(s, logit_of((uint32_t)(token >> 32)))) : 0;
+        const u64 w = live ? weight(token) : 0;
         u64 count = before_count, mass = before_mass;
         for (int i = 0; i < (int)n; ++i) {
             const bool ahead = lane_u64(token, i) >= token;
@@ -278,122 +316,296 @@ __device__ Place reach(Room &r, const Scale &s, const T *row, int vocab, bool by
     return p;
 }
 
+// The largest key of a slice, in every thread.
 template <class T>
-__global__ __launch_bounds__(kSampleThreads) void sample_kernel(const bq_draw a)
+__device__ __forceinline__ uint32_t slice_top(Room &r, const T *row, int lo, int hi)
 {
-    __shared__ Room r;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, vocab = (int)a.vocab;
-    for (int64_t at = blockIdx.x; at < a.rows; at += gridDim.x) {
-        const T *row = static_cast<const T *>(a.logits) + at * a.ld_logits;
-        uint32_t top = 0;
-        each_token(row, vocab, [&](int, float l) {
-            const uint32_t k = key_of(l);
-            top = k > top ? k : top;
-        });
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float top = -__builtin_inff();
+    each_token(row, lo, hi, [&](int, float l) { top = fmaxf(top, l); });  // (the number of a number and a NaN)
+    top = wave_all(top, Max());
+    if (lane == 0)
+        r.waves[0][wave] = key_of(top);
+    __syncthreads();
+    uint32_t key = 0;
+    for (int w = 0; w < kSampleThreads / 64; ++w)
+        key = (uint32_t)r.waves[0][w] > key ? (uint32_t)r.waves[0][w] : key;
+    __syncthreads();
+    return key;
+}
+
+// Counts and weights of a slice's tokens by bucket into r.count and r.mass; the weight of those that weigh at least
+// `least` (of 1), of the whole workgroup, in thread 0's return value.
+template <class T>
+__device__ __forceinline__ u64 slice_buckets(Room &r, const Scale &s, const T *row, int lo, int hi, double least)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    r.count[tid] = 0;
+    r.mass[tid] = 0;
+    __syncthreads();
+    const double bound = __builtin_ldexp(least, s.bits);
+    u64 over = 0;
+    each_token(row, lo, hi, [&](int, float l) {
+        if (!(l > -__builtin_inff()))
+            return;
+        const int b = bucket_of(s, l);
+        if (b >= kBuckets)
+            return;
+        const double w = weight_at(s, r.table, l);
+        const u64 units = rounded(w);
+        atomicAdd(&r.count[b], 1u);
+        atomicAdd(&r.mass[b], units);
+        over += w >= bound ? units : 0;
+    });
 #pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const uint32_t o = __shfl_xor(top, off, 64);
-            top = o > top ? o : top;
-        }
-        if (lane == 0)
-            r.waves[0][wave] = top;
-        r.count[tid] = 0;
-        r.mass[tid] = 0;
-        __syncthreads();
-        for (int w = 0; w < kSampleThreads / 64; ++w)
-            top = (uint32_t)r.waves[0][w] > top ? (uint32_t)r.waves[0][w] : top;
-        __syncthreads();
-        if (top == 0) {
-            if (tid == 0) {
-                a.token[at] = -1;
-                if (a.logprob)
-                    a.logprob[at] = -__builtin_inff();
-            }
-            continue;
-        }
-        const float t = a.temperature ? a.temperature[at] : 1.0f;
-        Scale s;
-        s.top = (double)logit_of(top);
-        s.greedy = !(t > 0.0f);
-        s.per = 1.44269504088896340736 / (double)t;
-        const int wide = 32 - __builtin_clz((unsigned)vocab);
-        s.bits = 62 - wide < 50 ? 62 - wide : 50;
-        s.buckets = (float)kBuckets / (float)(s.bits + 2);
-        const double least = a.min_p ? (double)a.min_p[at] : 0.0;
-        u64 over = 0;
-        each_token(row, vocab, [&](int, float l) {
-            if (!key_of(l))
-                return;
-            const double y = log2_weight(s, l);
-            const u64 w = weight_of(s, y);
-            if (!w)
-                return;
-            const int b = bucket_of(s, y);
-            atomicAdd(&r.count[b], 1u);
-            atomicAdd(&r.mass[b], w);
-            if (least > 0.0 && exp2(y) >= least)
-                over += w;
-        });
-        __syncthreads();
-        uint32_t c = r.count[tid];
-        u64 m = r.mass[tid];
-        scan(r, c, m);
-        r.count[tid] = c;
-        r.mass[tid] = m;
+    for (int off = 1; off < 64; off <<= 1)
+        over += __shfl_xor(over, off, 64);
+    if (lane == 0)
+        r.waves[0][wave] = over;
+    __syncthreads();
+    over = 0;
+    for (int w = 0; w < kSampleThreads / 64; ++w)
+        over += r.waves[0][w];
+    __syncthreads();
+    return over;
+}
+
+__device__ __forceinline__ void fill_table(Room &r)
+{
+    if (threadIdx.x < 32)
+        r.table[threadIdx.x] = exp2((double)threadIdx.x / 32.0);
+}
+
+// The rest of a row, whose counts and weights by bucket are in r.count and r.mass (`over`: the weight that min_p keeps).
+template <class T>
+__device__ void pick(Room &r, const bq_draw &a, const Scale &s, const T *row, int64_t at, u64 over)
+{
+    const int tid = threadIdx.x, vocab = (int)a.vocab;
+    uint32_t c = r.count[tid];
+    u64 m = r.mass[tid];
+    scan(r, c, m);
+    r.count[tid] = c;
+    r.mass[tid] = m;
+    __syncthreads();
+    const u64 total = r.mass[kBuckets - 1];
+    const uint32_t weighty = r.count[kBuckets - 1];
+    const int k = !s.greedy && a.top_k ? a.top_k[at] : 0;
+    const float p = !s.greedy && a.top_p ? a.top_p[at] : 1.0f;
+    const bool limit_k = k > 0 && (uint32_t)k < weighty, limit_p = p < 1.0f;
+    const double share = limit_p ? (double)p : 1.0;
+    // Two or three places are looked for, all within the first buckets: their tokens together, where the list has
+    // room.  Behind the bucket of the k-th token, or of a share p of all weight, nothing is looked at.
+    int known = -1;
+    if (limit_k || limit_p) {
         if (tid == 0)
-            r.answer = 0;
+            r.found = kBuckets - 1;
         __syncthreads();
-        if (over)
-            atomicAdd(&r.answer, over);
+        const u64 want = limit_k ? (u64)k : (u64)(share * (double)total) + 1;
+        const u64 upto = limit_k ? c : m;
+        if (upto >= want)
+            atomicMin(&r.found, (uint32_t)tid);
         __syncthreads();
-        over = r.answer;
-        const u64 total = r.mass[kBuckets - 1];
-        const uint32_t weighty = r.count[kBuckets - 1];
-        u64 mass = total;
-        if (!s.greedy) {
-            const int k = a.top_k ? a.top_k[at] : 0;
-            if (k > 0 && (uint32_t)k < weighty)
-                mass = reach(r, s, row, vocab, true, (u64)k).mass;
-            const float p = a.top_p ? a.top_p[at] : 1.0f;
-            if (p < 1.0f) {
-                const double want = (double)p * (double)mass;
-                u64 target = want > 0.0 ? (u64)__builtin_ceil(want) : 1;
-                target = target < 1 ? 1 : target > mass ? mass : target;
-                const u64 kept = reach(r, s, row, vocab, false, target).mass;
-                mass = kept < mass ? kept : mass;
-            }
-            if (least > 0.0)
-                mass = over < mass ? over : mass;
-        }
-        u64 target = 1;
-        if (!s.greedy && mass) {
-            const double want = (double)a.u[at] * (double)mass;
-            target = want >= 1.0 ? (want >= (double)mass ? mass : (u64)want + 1) : 1;
-            target = target > mass ? mass : target;
-        }
-        const Place p = reach(r, s, row, vocab, false, target);
-        if (tid == 0) {
-            a.token[at] = (uint32_t)~(uint32_t)p.token;
-            if (a.logprob) {
-                const double y = log2_weight(s, logit_of((uint32_t)(p.token >> 32)));
-                a.logprob[at] = s.greedy ? 0.0f
-                                         : (float)(y * 0.69314718055994530942 - log(__builtin_ldexp((double)total, -s.bits)));
-            }
+        const int last = (int)r.found;
+        if (r.count[last] <= kList) {
+            known = last;
+            if (tid == 0)
+                r.listed = 0;
+            __syncthreads();
+            each_token(row, 0, vocab, [&](int i, float l) {
+                if (l > -__builtin_inff() && bucket_of(s, l) <= last) {
+                    const uint32_t to = atomicAdd(&r.listed, 1u);
+                    if (to < kList)
+                        r.list[to] = token_of(l, i);
+                }
+            });
         }
         __syncthreads();
     }
+    u64 mass = total;
+    if (limit_k)
+        mass = reach(r, s, row, vocab, true, (u64)k, known).mass;
+    if (limit_p) {
+        const double want = share * (double)mass;
+        u64 target = want > 0.0 ? (u64)__builtin_ceil(want) : 1;
+        target = target < 1 ? 1 : target > mass ? mass : target;
+        const u64 kept = reach(r, s, row, vocab, false, target, known).mass;
+        mass = kept < mass ? kept : mass;
+    }
+    if (!s.greedy)
+        mass = over < mass ? over : mass;
+    u64 target = 1;
+    if (!s.greedy && mass) {
+        const double want = (double)a.u[at] * (double)mass;
+        target = want >= 1.0 ? (want >= (double)mass ? mass : (u64)want + 1) : 1;
+        target = target > mass ? mass : target;
+    }
+    const Place place = reach(r, s, row, vocab, false, target, known);
+    if (tid == 0) {
+        a.token[at] = (uint32_t)~(uint32_t)place.token;
+        if (a.logprob) {
+            const double w = weight_at(s, r.table, logit_of((uint32_t)(place.token >> 32)));
+            a.logprob[at] = s.greedy ? 0.0f : (float)log(w / (double)total);
+        }
+    }
+    __syncthreads();
 }
 
-int64_t sample_work(const bq_draw &) { return 0; }
+__device__ __forceinline__ double least_of(const bq_draw &a, const Scale &s, int64_t at)
+{
+    const float least = a.min_p && !s.greedy ? a.min_p[at] : 0.0f;
+    return least > 0.0f ? (double)least : 0.0;
+}
+__device__ __forceinline__ void no_token(const bq_draw &a, int64_t at)
+{
+    if (threadIdx.x == 0) {
+        a.token[at] = -1;
+        if (a.logprob)
+            a.logprob[at] = -__builtin_inff();
+    }
+}
+
+// Whole rows, one a workgroup at a time.
+template <class T>
+__global__ __launch_bounds__(kSampleThreads) void sample_rows(const bq_draw a)
+{
+    __shared__ Room r;
+    fill_table(r);
+    for (int64_t at = blockIdx.x; at < a.rows; at += gridDim.x) {
+        const T *row = static_cast<const T *>(a.logits) + at * a.ld_logits;
+        const uint32_t top = slice_top(r, row, 0, (int)a.vocab);
+        if (top == 0) {
+            no_token(a, at);
+            continue;
+        }
+        const Scale s = scale_of_row(top, a.temperature ? a.temperature[at] : 1.0f, (int)a.vocab);
+        const u64 over = slice_buckets(r, s, row, 0, (int)a.vocab, least_of(a, s, at));
+        pick(r, a, s, row, at, over);
+    }
+}
+
+// Few rows: their slices in three launches, with what the launches hand on in scratch: a key a slice, then a slice's
+// 1024 weights, 1024 counts and what min_p keeps.
+struct Slices {
+    bq_draw a;
+    int n, len;  // slices a row, tokens a slice
+};
+constexpr int64_t kSliceBytes = kBuckets * 12 + 16;
+__device__ __forceinline__ uint32_t *slice_keys(const Slices &g, int64_t at) { return static_cast<uint32_t *>(g.a.work) + at * g.n; }
+__device__ __forceinline__ u64 *slice_sums(const Slices &g, int64_t at, int i)
+{
+    const int64_t keys = (g.a.rows * g.n * 4 + 15) / 16 * 16;
+    return reinterpret_cast<u64 *>(static_cast<char *>(g.a.work) + keys + (at * g.n + i) * kSliceBytes);
+}
+__device__ __forceinline__ uint32_t row_top(const Slices &g, int64_t at)
+{
+    uint32_t top = 0;
+    for (int i = 0; i < g.n; ++i)
+        top = slice_keys(g, at)[i] > top ? slice_keys(g, at)[i] : top;
+    return top;
+}
+
+template <class T>
+__global__ __launch_bounds__(kSampleThreads) void sample_tops(const Slices g)
+{
+    __shared__ Room r;
+    const int64_t at = blockIdx.x / g.n;
+    const int i = blockIdx.x % g.n, lo = i * g.len, hi = lo + g.len < g.a.vocab ? lo + g.len : (int)g.a.vocab;
+    const uint32_t top = slice_top(r, static_cast<const T *>(g.a.logits) + at * g.a.ld_logits, lo, hi);
+    if (threadIdx.x == 0)
+        slice_keys(g, at)[i] = top;
+}
+
+template <class T>
+__global__ __launch_bounds__(kSampleThreads) void sample_buckets(const Slices g)
+{
+    __shared__ Room r;
+    fill_table(r);
+    const bq_draw &a = g.a;
+    const int tid = threadIdx.x;
+    const int64_t at = blockIdx.x / g.n;
+    const int i = blockIdx.x % g.n, lo = i * g.len, hi = lo + g.len < a.vocab ? lo + g.len : (int)a.vocab;
+    const uint32_t top = row_top(g, at);
+    if (top == 0)
+        return;
+    const Scale s = scale_of_row(top, a.temperature ? a.temperature[at] : 1.0f, (int)a.vocab);
+    const u64 over = slice_buckets(r, s, static_cast<const T *>(a.logits) + at * a.ld_logits, lo, hi, least_of(a, s, at));
+    u64 *sums = slice_sums(g, at, i);
+    sums[tid] = r.mass[tid];
+    reinterpret_cast<uint32_t *>(sums + kBuckets)[tid] = r.count[tid];
+    if (tid == 0)
+        sums[kBuckets + kBuckets / 2] = over;
+}
+
+template <class T>
+__global__ __launch_bounds__(kSampleThreads) void sample_pick(const Slices g)
+{
+    __shared__ Room r;
+    fill_table(r);
+    const bq_draw &a = g.a;
+    const int tid = threadIdx.x;
+    const int64_t at = blockIdx.x;
+    const uint32_t top = row_top(g, at);
+    if (top == 0) {
+        no_token(a, at);
+        return;
+    }
+    const Scale s = scale_of_row(top, a.temperature ? a.temperature[at] : 1.0f, (int)a.vocab);
+    u64 mass = 0, over = 0;
+    uint32_t count = 0;
+#pragma unroll 8
+    for (int i = 0; i < g.n; ++i) {
+        const u64 *sums = slice_sums(g, at, i);
+        mass += sums[tid];
+        count += reinterpret_cast<const uint32_t *>(sums + kBuckets)[tid];
+        over += sums[kBuckets + kBuckets / 2];
+    }
+    r.mass[tid] = mass;
+    r.count[tid] = count;
+    __syncthreads();
+    pick(r, a, s, static_cast<const T *>(a.logits) + at * a.ld_logits, at, over);
+}
+
+// Slices a row: enough workgroups for two a compute unit, each with 4096 tokens or more; 1: whole rows.
+static Slices slices_of(const bq_draw &a)
+{
+    Slices g;
+    g.a = a;
+    int64_t n = 512 / a.rows;
+    const int64_t most = (a.vocab + 4095) / 4096 < 32 ? (a.vocab + 4095) / 4096 : 32;
+    n = n < 1 ? 1 : n > most ? most : n;
+    g.len = (int)((a.vocab + n - 1) / n);
+    g.n = (int)((a.vocab + g.len - 1) / g.len);
+    return g;
+}
+
+int64_t sample_work(const bq_draw &a)
+{
+    const Slices g = slices_of(a);
+    return g.n == 1 ? 0 : (a.rows * g.n * 4 + 15) / 16 * 16 + a.rows * g.n * kSliceBytes;
+}
+
+template <class T>
+static void sample_type(const bq_draw &a, hipStream_t st)
+{
+    const Slices g = slices_of(a);
+    const dim3 block(kSampleThreads);
+    if (g.n == 1) {
+        const int64_t most = int64_t(1) << 21;
+        hipLaunchKernelGGL((sample_rows<T>), dim3((unsigned)(a.rows < most ? a.rows : most)), block, 0, st, a);
+        return;
+    }
+    const dim3 grid((unsigned)(a.rows * g.n));
+    hipLaunchKernelGGL((sample_tops<T>), grid, block, 0, st, g);
+    hipLaunchKernelGGL((sample_buckets<T>), grid, block, 0, st, g);
+    hipLaunchKernelGGL((sample_pick<T>), dim3((unsigned)a.rows), block, 0, st, g);
+}
 
 hipError_t launch_sample(const bq_draw &a, hipStream_t st)
 {
-    const int64_t most = int64_t(1) << 21;
-    const dim3 grid((unsigned)(a.rows < most ? a.rows : most)), block(kSampleThreads);
     switch (a.type) {
-    case BQ_F16: hipLaunchKernelGGL((sample_kernel<_Float16>), grid, block, 0, st, a); break;
-    case BQ_BF16: hipLaunchKernelGGL((sample_kernel<__bf16>), grid, block, 0, st, a); break;
-    default: hipLaunchKernelGGL((sample_kernel<float>), grid, block, 0, st, a); break;
+    case BQ_F16: sample_type<_Float16>(a, st); break;
+    case BQ_BF16: sample_type<__bf16>(a, st); break;
+    default: sample_type<float>(a, st); break;
     }
     return hipGetLastError();
 }
