@@ -12,13 +12,41 @@ namespace bq {
 
 constexpr int kGatedThreads = 256;
 
+// exp(x) for |x| of any size: 2^(n / 32) with n the nearest integer to 32 x log2(e), the rest (at most ln 2 / 64) by its
+// series (the first term left out is below 2^-56), 2^(n % 32 / 32) from a table in LDS; n is held to where the result is
+// past every f32 that could matter (x of +-1500: 1 + exp is 1 or infinite against any product of two f32).
+__device__ __forceinline__ double exp_of(const double *table, double x)
+{
+    const double y = fmin(fmax(x, -1500.0), 1500.0) * (32.0 * 1.44269504088896340736), n = __builtin_rint(y);
+    // ln 2 / 32 in two parts, the first with zeros at its end: n times it is exact
+    const double f = __builtin_fma(n, -1.0 * 0x1.62e42fefa0000p-6, fmin(fmax(x, -1500.0), 1500.0)) - n * 0x1.cf79abc9e3b3ap-45;
+    double p = 1.0 / 720.0;
+    p = __builtin_fma(p, f, 1.0 / 120.0);
+    p = __builtin_fma(p, f, 1.0 / 24.0);
+    p = __builtin_fma(p, f, 1.0 / 6.0);
+    p = __builtin_fma(p, f, 0.5);
+    p = __builtin_fma(p, f, 1.0);
+    p = __builtin_fma(p, f, 1.0);
+    const int i = (int)n;
+    return __builtin_ldexp(p * table[i & 31], i >> 5);
+}
+// x / d for d >= 1 (or infinite) to the last bit but one: the reciprocal's 2^-23 or better, squared twice.
+__device__ __forceinline__ double over(double x, double d)
+{
+    double r = __builtin_amdgcn_rcp(d);
+    r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+    r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+    const double q = x * r;
+    return __builtin_copysign(d > 1e300 ? 0.0 : __builtin_fma(__builtin_fma(-d, q, x), r, q), x);  // -0 stays so
+}
+
 template <int ACT>
-__device__ __forceinline__ double activate(double x)
+__device__ __forceinline__ double activate(const double *table, double x)
 {
     if constexpr (ACT == BQ_SILU)
-        return x / (1.0 + exp(-x));
+        return over(x, 1.0 + exp_of(table, -x));
     else if constexpr (ACT == BQ_GELU)  // 1.5957691216 = 2 sqrt(2 / pi)
-        return x / (1.0 + exp(-1.5957691216057307117 * __builtin_fma(0.044715 * x * x, x, x)));
+        return over(x, 1.0 + exp_of(table, -1.5957691216057307117 * __builtin_fma(0.044715 * x * x, x, x)));
     else if constexpr (ACT == BQ_RELU2)
         return x > 0.0 ? x * x : 0.0;
     else
@@ -28,6 +56,12 @@ __device__ __forceinline__ double activate(double x)
 template <class T, int ACT>
 __global__ __launch_bounds__(kGatedThreads) void gated_kernel(const bq_gated a)
 {
+    __shared__ double table[32];  // 2^(i / 32)
+    if (ACT == BQ_SILU || ACT == BQ_GELU) {
+        if (threadIdx.x < 32)
+            table[threadIdx.x] = exp2((double)threadIdx.x / 32.0);
+        __syncthreads();
+    }
     const int per_row = (int)(a.n / 8);
     const int64_t total = a.tokens * per_row;
     const int log2 = __builtin_ctz((unsigned)a.qa);
@@ -46,7 +80,7 @@ __global__ __launch_bounds__(kGatedThreads) void gated_kernel(const bq_gated a)
             load8(static_cast<const T *>(a.up) + t * a.ld_up + i, u);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                v[e] = (float)(activate<ACT>((double)g[e]) * (double)u[e]);
+                v[e] = (float)(activate<ACT>(table, (double)g[e]) * (double)u[e]);
                 m = fmaxf(m, fabsf(v[e]));
             }
         }
@@ -73,8 +107,8 @@ static void gated_type(const bq_gated &a, dim3 grid, hipStream_t st)
 
 hipError_t launch_gated(const bq_gated &a, hipStream_t st)
 {
-    // a grid holds fewer than 2^32 threads; workgroups walk on from there
-    const int64_t blocks = (a.tokens * (a.n / 8) + kGatedThreads - 1) / kGatedThreads, most = int64_t(1) << 22;
+    const int64_t blocks = (a.tokens * (a.n / 8) + kGatedThreads - 1) / kGatedThreads, most = 2048;
+    // eight workgroups a compute unit, which walk on: the table once for many pieces
     const dim3 grid((unsigned)(blocks < most ? blocks : most));
     switch (a.type) {
     case BQ_F16: gated_type<_Float16>(a, grid, st); break;

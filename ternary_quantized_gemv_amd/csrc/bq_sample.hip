@@ -67,6 +67,12 @@ __device__ __forceinline__ int bucket_of(const Scale &s, float l)
     const float x = (s.topf - l) * s.buckets;
     return !s.greedy && x < (float)kBuckets ? (int)x : kBuckets;
 }
+// Every logit of buckets 0 .. b is at least this (the slack is far above what bucket_of's roundings come to; a NaN, from
+// infinite operands, is above nothing).
+__device__ __forceinline__ float least_logit(const Scale &s, int b)
+{
+    return s.topf - (float)(b + 1) / s.buckets * 1.0001f - fabsf(s.topf) * 0x1p-20f;
+}
 // exp((l - top) / T) in units of 2^-bits, before it is rounded: 2^(y / 32) with y = n + f, |f| <= 1/2, of which 2^(f / 32)
 // is exp(f ln 2 / 32) by its series (the first term left out is below 2^-48 of it), and 2^(n % 32 / 32) from a table.
 __device__ __forceinline__ double weight_at(const Scale &s, const double *table, float l)
@@ -106,7 +112,7 @@ struct Room {
     u64 waves[2][kSampleThreads / 64];
     uint32_t found;
     u64 before_count, before_mass, low, high, answer;
-    uint32_t listed;
+    uint32_t listed, gathered;
 };
 
 // Running sums over all threads' count and mass (inclusive); every thread gets its own.
@@ -137,9 +143,20 @@ __device__ __forceinline__ void scan(Room &r, uint32_t &count, u64 &mass)
     __syncthreads();
 }
 
-// Calls f(index, logit) once for each token from lo to hi of a row: 16 bytes a load, four loads under way.
-template <class T, class F>
-__device__ __forceinline__ void each_token(const T *row, int lo, int hi, F f)
+template <int V, class VEC>
+__device__ __forceinline__ float largest(const VEC &v)
+{
+    float m = (float)v[0];
+#pragma unroll
+    for (int e = 1; e < V; ++e)
+        m = fmaxf(m, (float)v[e]);
+    return m;
+}
+
+// Calls f(index, logit) once for each token from lo to hi of a row: 16 bytes a load, LOADS of them under way.  Where all
+// of a load's logits are below `least`, they may be left out.
+template <int LOADS, class T, class F>
+__device__ __forceinline__ void each_token(const T *row, int lo, int hi, float least, F f)
 {
     constexpr int V = 16 / sizeof(T);
     typedef T vec __attribute__((ext_vector_type(V)));
@@ -151,16 +168,17 @@ __device__ __forceinline__ void each_token(const T *row, int lo, int hi, F f)
     const int from = lo + head, n = (hi - from) / V;
     const vec *p = reinterpret_cast<const vec *>(row + from);
     int c = tid;
-    for (; c + 3 * kSampleThreads < n; c += 4 * kSampleThreads) {
-        vec v[4];
+    for (; c + (LOADS - 1) * kSampleThreads < n; c += LOADS * kSampleThreads) {
+        vec v[LOADS];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < LOADS; ++j)
             v[j] = p[c + j * kSampleThreads];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < LOADS; ++j)
+            if (!(largest<V>(v[j]) < least))
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                f(from + (c + j * kSampleThreads) * V + e, (float)v[j][e]);
+                for (int e = 0; e < V; ++e)
+                    f(from + (c + j * kSampleThreads) * V + e, (float)v[j][e]);
     }
     for (; c < n; c += kSampleThreads) {
         const vec v = p[c];
@@ -179,28 +197,37 @@ struct Place {
     u64 token;  // (key, ~index)
 };
 
-// The first token at which the running count (by_count) or weight reaches target, which
-// the whole row does (1 <= target).  The tokens of buckets 0 .. known are in the list already
-// (known < 0: none).
-template <class T>
-__device__ Place reach(Room &r, const Scale &s, const T *row, int vocab, bool by_count, u64 target, int known)
+// The bucket in which the running count (by_count) or weight reaches target, and the sums in front of it.
+struct Found {
+    int bucket;
+    u64 count, mass;
+};
+__device__ __forceinline__ Found find(Room &r, bool by_count, u64 target)
 {
     const int tid = threadIdx.x;
-    {
-        const u64 upto = by_count ? r.count[tid] : r.mass[tid], before = tid ? (by_count ? r.count[tid - 1] : r.mass[tid - 1]) : 0;
-        if (before < target && target <= upto) {
-            r.found = tid;
-            r.before_count = tid ? r.count[tid - 1] : 0;
-            r.before_mass = tid ? r.mass[tid - 1] : 0;
-        }
-    }
+    const u64 upto = by_count ? r.count[tid] : r.mass[tid], before = tid ? (by_count ? r.count[tid - 1] : r.mass[tid - 1]) : 0;
+    if (before < target && target <= upto)
+        r.found = tid;
     __syncthreads();
-    const int bucket = (int)r.found;
-    u64 n = r.count[bucket] - (uint32_t)r.before_count, before_count = r.before_count, before_mass = r.before_mass;
+    const int b = (int)r.found;
+    const Found f{b, b ? r.count[b - 1] : 0, b ? r.mass[b - 1] : 0};
+    __syncthreads();
+    return f;
+}
+
+// The first token at which the running count (by_count) or weight reaches target, which
+// the whole row does (1 <= target).  gathered: the list holds all tokens of its bucket.
+template <class T>
+__device__ __forceinline__ Place reach(Room &r, const Scale &s, const T *row, int vocab, bool by_count, u64 target, bool gathered)
+{
+    const int tid = threadIdx.x;
+    const Found found = find(r, by_count, target);
+    const int bucket = found.bucket;
+    u64 before_count = found.count, before_mass = found.mass, n = r.count[bucket] - before_count;
     // tokens low <= (key, ~index) <= high of the bucket: n of them, the target among them
     u64 low = 0, high = ~0ull;
-    bool from_list = bucket <= known;
-    int listed = from_list ? (int)r.count[known] : 0;
+    bool from_list = gathered;
+    int listed = gathered ? (int)r.gathered : 0;
     auto weight = [&](u64 token) { return rounded(weight_at(s, r.table, logit_of((uint32_t)(token >> 32)))); };
     auto member = [&](u64 token) {
         return token >= low && token <= high && bucket_of(s, logit_of((uint32_t)(token >> 32))) == bucket;
@@ -211,7 +238,7 @@ __device__ Place reach(Room &r, const Scale &s, const T *row, int vocab, bool by
                 if (member(r.list[i]))
                     f(r.list[i]);
         } else {
-            each_token(row, 0, vocab, [&](int i, float l) {
+            each_token<4>(row, 0, vocab, least_logit(s, bucket), [&](int i, float l) {
                 if (l > -__builtin_inff() && bucket_of(s, l) == bucket) {
                     const u64 token = token_of(l, i);
                     if (token >= low && token <= high)
@@ -252,7 +279,13 @@ __device__ Place reach(Room &r, const Scale &s, const T *row, int vocab, bool by
                 lo = token < lo ? token : lo;
                 hi = token > hi ? token : hi;
             });
-            if (lo <= hi) {
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const u64 l = __shfl_xor(lo, off, 64), h = __shfl_xor(hi, off, 64);
+                lo = l < lo ? l : lo;
+                hi = h > hi ? h : hi;
+            }
+            if ((tid & 63) == 0 && lo <= hi) {
                 atomicMin(&r.low, lo);
                 atomicMax(&r.high, hi);
             }
@@ -322,7 +355,7 @@ __device__ __forceinline__ uint32_t slice_top(Room &r, const T *row, int lo, int
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float top = -__builtin_inff();
-    each_token(row, lo, hi, [&](int, float l) { top = fmaxf(top, l); });  // (the number of a number and a NaN)
+    each_token<4>(row, lo, hi, -__builtin_inff(), [&](int, float l) { top = fmaxf(top, l); });  // (the number of a number and a NaN)
     top = wave_all(top, Max());
     if (lane == 0)
         r.waves[0][wave] = key_of(top);
@@ -345,7 +378,7 @@ __device__ __forceinline__ u64 slice_buckets(Room &r, const Scale &s, const T *r
     __syncthreads();
     const double bound = __builtin_ldexp(least, s.bits);
     u64 over = 0;
-    each_token(row, lo, hi, [&](int, float l) {
+    each_token<2>(row, lo, hi, least_logit(s, kBuckets - 1), [&](int, float l) {
         if (!(l > -__builtin_inff()))
             return;
         const int b = bucket_of(s, l);
@@ -393,53 +426,76 @@ __device__ void pick(Room &r, const bq_draw &a, const Scale &s, const T *row, in
     const float p = !s.greedy && a.top_p ? a.top_p[at] : 1.0f;
     const bool limit_k = k > 0 && (uint32_t)k < weighty, limit_p = p < 1.0f;
     const double share = limit_p ? (double)p : 1.0;
-    // Two or three places are looked for, all within the first buckets: their tokens together, where the list has
-    // room.  Behind the bucket of the k-th token, or of a share p of all weight, nothing is looked at.
-    int known = -1;
-    if (limit_k || limit_p) {
-        if (tid == 0)
-            r.found = kBuckets - 1;
-        __syncthreads();
-        const u64 want = limit_k ? (u64)k : (u64)(share * (double)total) + 1;
-        const u64 upto = limit_k ? c : m;
-        if (upto >= want)
-            atomicMin(&r.found, (uint32_t)tid);
-        __syncthreads();
-        const int last = (int)r.found;
-        if (r.count[last] <= kList) {
-            known = last;
-            if (tid == 0)
-                r.listed = 0;
-            __syncthreads();
-            each_token(row, 0, vocab, [&](int i, float l) {
-                if (l > -__builtin_inff() && bucket_of(s, l) <= last) {
-                    const uint32_t to = atomicAdd(&r.listed, 1u);
-                    if (to < kList)
-                        r.list[to] = token_of(l, i);
-                }
-            });
-        }
-        __syncthreads();
-    }
-    u64 mass = total;
-    if (limit_k)
-        mass = reach(r, s, row, vocab, true, (u64)k, known).mass;
-    if (limit_p) {
+    // How far each filter's place, and the draw's, can lie apart follows from the buckets: their tokens are collected
+    // in one pass over the row, where the list has room for them (else each place is looked for in a pass of its own).
+    auto share_of = [&](u64 mass) {
         const double want = share * (double)mass;
-        u64 target = want > 0.0 ? (u64)__builtin_ceil(want) : 1;
-        target = target < 1 ? 1 : target > mass ? mass : target;
-        const u64 kept = reach(r, s, row, vocab, false, target, known).mass;
-        mass = kept < mass ? kept : mass;
+        const u64 target = want > 0.0 ? (u64)__builtin_ceil(want) : 1;
+        return target < 1 ? 1 : target > mass ? mass : target;
+    };
+    const double u = s.greedy ? 0.0 : (double)a.u[at];
+    auto drawn_of = [&](u64 mass) {
+        const double want = u * (double)mass;
+        const u64 target = want >= 1.0 ? (want >= (double)mass ? mass : (u64)want + 1) : 1;
+        return target > mass && mass ? mass : target;
+    };
+    u64 lo = total, hi = total;  // bounds of the kept weight
+    int k0 = 0, k1 = -1, p0 = 0, p1 = -1;
+    if (limit_k) {
+        const Found f = find(r, true, (u64)k);
+        k0 = k1 = f.bucket;
+        lo = f.mass;
+        hi = r.mass[k0];
     }
-    if (!s.greedy)
-        mass = over < mass ? over : mass;
-    u64 target = 1;
-    if (!s.greedy && mass) {
-        const double want = (double)a.u[at] * (double)mass;
-        target = want >= 1.0 ? (want >= (double)mass ? mass : (u64)want + 1) : 1;
-        target = target > mass ? mass : target;
+    if (limit_p) {
+        const Found f = find(r, false, share_of(lo)), g = find(r, false, share_of(hi));
+        p0 = f.bucket;
+        p1 = g.bucket;
+        lo = f.mass < lo ? f.mass : lo;
+        hi = r.mass[p1] < hi ? r.mass[p1] : hi;
     }
-    const Place place = reach(r, s, row, vocab, false, target, known);
+    if (!s.greedy) {
+        lo = over < lo ? over : lo;
+        hi = over < hi ? over : hi;
+    }
+    const int d0 = find(r, false, drawn_of(lo)).bucket, d1 = find(r, false, drawn_of(hi)).bucket;
+    auto counted = [&](int from, int to) { return from > to ? 0u : r.count[to] - (from ? r.count[from - 1] : 0u); };
+    const bool gather = counted(k0, k1) + counted(p0, p1) + counted(d0, d1) <= kList;
+    if (gather) {
+        if (tid == 0)
+            r.gathered = 0;
+        __syncthreads();
+        each_token<8>(row, 0, vocab, least_logit(s, d1 > p1 ? d1 > k1 ? d1 : k1 : p1 > k1 ? p1 : k1), [&](int i, float l) {
+            if (!(l > -__builtin_inff()))
+                return;
+            const int b = bucket_of(s, l);
+            if ((b >= d0 && b <= d1) || (b >= p0 && b <= p1) || b == k1) {
+                const uint32_t to = atomicAdd(&r.gathered, 1u);
+                if (to < kList)
+                    r.list[to] = token_of(l, i);
+            }
+        });
+        __syncthreads();
+        if (tid == 0 && r.gathered > kList)  // (only if something changes the logits meanwhile)
+            r.gathered = kList;
+        __syncthreads();
+    }
+    // the places in turn: the k-th token, the end of top_p, the draw
+    u64 mass = total, target = 1;
+    Place place;
+    for (int what = limit_k ? 0 : limit_p ? 1 : 2;; what = what == 0 && limit_p ? 1 : 2) {
+        if (what == 1)
+            target = share_of(mass);
+        if (what == 2) {
+            if (!s.greedy)
+                mass = over < mass ? over : mass;
+            target = drawn_of(mass);
+        }
+        place = reach(r, s, row, vocab, what == 0, what == 0 ? (u64)k : target, gather);
+        if (what == 2)
+            break;
+        mass = place.mass < mass ? place.mass : mass;
+    }
     if (tid == 0) {
         a.token[at] = (uint32_t)~(uint32_t)place.token;
         if (a.logprob) {
@@ -571,7 +627,7 @@ static Slices slices_of(const bq_draw &a)
     Slices g;
     g.a = a;
     int64_t n = 512 / a.rows;
-    const int64_t most = (a.vocab + 4095) / 4096 < 32 ? (a.vocab + 4095) / 4096 : 32;
+    const int64_t most = (a.vocab + 4095) / 4096 < 16 ? (a.vocab + 4095) / 4096 : 16;
     n = n < 1 ? 1 : n > most ? most : n;
     g.len = (int)((a.vocab + n - 1) / n);
     g.n = (int)((a.vocab + g.len - 1) / g.len);
