@@ -71,6 +71,8 @@ __device__ __forceinline__ int bucket_of(const Scale &s, float l)
 // infinite operands, is above nothing).
 __device__ __forceinline__ float least_logit(const Scale &s, int b)
 {
+    if (s.greedy)
+        return s.topf;
     return s.topf - (float)(b + 1) / s.buckets * 1.0001f - fabsf(s.topf) * 0x1p-20f;
 }
 // exp((l - top) / T) in units of 2^-bits, before it is rounded: 2^(y / 32) with y = n + f, |f| <= 1/2, of which 2^(f / 32)
@@ -191,6 +193,42 @@ __device__ __forceinline__ void each_token(const T *row, int lo, int hi, float l
         f(rest, (float)row[rest]);
 }
 
+// Calls f(index, logit) for the tokens of a row whose logit is not below `least`, and maybe others; few of them: what a
+// load brings is only compared, and read again where there is one.
+template <class T, class F>
+__device__ __forceinline__ void each_above(const T *row, int vocab, float least, F f)
+{
+    constexpr int V = 16 / sizeof(T), LOADS = 8;
+    typedef T vec __attribute__((ext_vector_type(V)));
+    const int tid = threadIdx.x;
+    int head = (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(T);
+    head = head < vocab ? head : vocab;
+    const int n = (vocab - head) / V, ends = vocab - n * V;
+    const vec *p = reinterpret_cast<const vec *>(row + head);
+    for (int c = tid; c < n; c += LOADS * kSampleThreads) {
+        vec v[LOADS];
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j)
+            v[j] = p[c + j * kSampleThreads < n ? c + j * kSampleThreads : c];
+        uint32_t some = 0;
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j)
+            some |= c + j * kSampleThreads < n && !(largest<V>(v[j]) < least) ? 1u << j : 0;
+        while (some) {
+            const int j = __builtin_ctz(some), first = head + (c + j * kSampleThreads) * V;
+            some &= some - 1;
+#pragma unroll 1
+            for (int e = 0; e < V; ++e)
+                f(first + e, (float)row[first + e]);
+        }
+    }
+    // what no whole load holds, at both ends
+    if (tid < ends) {
+        const int i = tid < head ? tid : n * V + tid;
+        f(i, (float)row[i]);
+    }
+}
+
 // A place of the descending order: the sum of weights up to and with its token.
 struct Place {
     u64 mass;
@@ -238,7 +276,7 @@ __device__ __forceinline__ Place reach(Room &r, const Scale &s, const T *row, in
                 if (member(r.list[i]))
                     f(r.list[i]);
         } else {
-            each_token<4>(row, 0, vocab, least_logit(s, bucket), [&](int i, float l) {
+            each_above(row, vocab, least_logit(s, bucket), [&](int i, float l) {
                 if (l > -__builtin_inff() && bucket_of(s, l) == bucket) {
                     const u64 token = token_of(l, i);
                     if (token >= low && token <= high)
@@ -465,7 +503,8 @@ __device__ void pick(Room &r, const bq_draw &a, const Scale &s, const T *row, in
         if (tid == 0)
             r.gathered = 0;
         __syncthreads();
-        each_token<8>(row, 0, vocab, least_logit(s, d1 > p1 ? d1 > k1 ? d1 : k1 : p1 > k1 ? p1 : k1), [&](int i, float l) {
+        const int most = d1 > p1 ? d1 > k1 ? d1 : k1 : p1 > k1 ? p1 : k1;
+        auto collect = [&](int i, float l) {
             if (!(l > -__builtin_inff()))
                 return;
             const int b = bucket_of(s, l);
@@ -474,7 +513,12 @@ __device__ void pick(Room &r, const bq_draw &a, const Scale &s, const T *row, in
                 if (to < kList)
                     r.list[to] = token_of(l, i);
             }
-        });
+        };
+        // few tokens that far up in the order: most loads hold none of them
+        if (r.count[most] < (uint32_t)vocab / 64)
+            each_above(row, vocab, least_logit(s, most), collect);
+        else
+            each_token<16 / sizeof(T)>(row, 0, vocab, -__builtin_inff(), collect);
         __syncthreads();
         if (tid == 0 && r.gathered > kList)  // (only if something changes the logits meanwhile)
             r.gathered = kList;

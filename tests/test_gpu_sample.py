@@ -116,8 +116,14 @@ def test_greedy_and_temperatures():
     x[3, 17], x[3, 18] = float("inf"), float("inf")
     token, logprob = run(x.cuda(), [0.99] * 6, temperature=[0.0, -1.0, float("nan"), 0.0, 1e-30, 1e-38], top_k=[5] * 6, top_p=[0.5] * 6)
     assert token.tolist()[:4] == [1234, 1234, 1234, 17] and (logprob[:4] == 0).all()
+    small, lp = token, logprob
+    # rows long enough to be read several loads at a time, the largest anywhere
+    g = np.random.default_rng(1)
+    long = t.from_numpy(g.standard_normal((40, 70001)).astype(np.float32))
+    token, _ = run(long.cuda(), [0.7] * 40, temperature=[[0.0, -2.0, float("nan"), -0.0][i % 4] for i in range(40)])
+    assert token.tolist() == long.argmax(1).tolist()
     # a tiny temperature leaves the largest, each a third
-    assert all(v in (1234, 3000) for v in token[4:]) and np.allclose(logprob[4:], np.log(1 / 3), rtol=1e-6)
+    assert all(v in (1234, 3000) for v in small[4:]) and np.allclose(lp[4:], np.log(1 / 3), rtol=1e-6)
     # an infinite one all alike
     token, logprob = run(x[:1].cuda(), [0.5], temperature=[float("inf")])
     order = Ranked(x[0].numpy()).order
