@@ -16,9 +16,10 @@ from . import (Act, BQ_Q1_0, GroupCall, Weights, bq_q1_0_matvec, bq_q2_0_matvec,
                bq_quantize_act_q8_f16, bq_sweep_create, bq_sweep_create_x, bq_token_sweep, BLOCK_LEN)
 
 try:
-    from . import bq_adapters_add, bq_kv_append, bq_paged_attn, bq_rmsnorm_q8
+    from . import (BQ_SILU, bq_adapters_add, bq_embed, bq_gated_q8, bq_kv_append, bq_matmul, bq_matmul_work_bytes,
+                   bq_paged_attn, bq_rmsnorm_q8, bq_sample, bq_sample_work_bytes)
 except ImportError:  # no torch: what lists the products works without it
-    pass
+    BQ_SILU = 1
 
 
 class StagedSweep:
@@ -206,6 +207,35 @@ class StagedChain:
         self.stages = []
 
 
+# --------------------------------------------------------------- products
+class _Products:
+    """Products of any number of tokens: 16 columns a call, or one bq_matmul
+    from matmul_from tokens on, whose scratch is allocated here."""
+
+    COLUMNS = 16  # activation columns of one product call
+
+    def __init__(self, fmt: int, weights, qa: int, max_tokens: int, matmul_from, device):
+        self.fmt, self.qa, self.matmul_from, self.work = fmt, qa, matmul_from, None
+        if matmul_from is not None and max_tokens >= matmul_from:
+            import torch
+            # more tokens need more scratch
+            need = max(bq_matmul_work_bytes(w, max_tokens, qa) for w in weights)
+            self.work = torch.empty(need, dtype=torch.uint8, device=device)
+
+    def wide(self, tokens: int) -> bool:
+        return self.matmul_from is not None and tokens >= self.matmul_from
+
+    def __call__(self, w, act, d, y, tokens: int, stream, res=None):
+        """y = W x (+ res, with wide() only) for the first rows of act, d and y."""
+        if self.wide(tokens):
+            bq_matmul(w, Act(act[:tokens], d[:tokens], w.cols, self.qa, tokens), y[:tokens], res=res, work=self.work, stream=stream)
+            return
+        call = bq_q1_0_matvec if self.fmt == BQ_Q1_0 else bq_q2_0_matvec
+        for c in range(0, tokens, self.COLUMNS):
+            e = min(tokens, c + self.COLUMNS)
+            call(w, Act(act[c:e], d[c:e], w.cols, self.qa, e - c), y[c:e], stream)
+
+
 # --------------------------------------------------------------- attention
 class StagedAttention:
     """The attention block of a decoder layer between its packed products, for
@@ -219,12 +249,16 @@ class StagedAttention:
     device, so that run() allocates nothing and can be captured into a graph;
     run() of two blocks on two streams need two objects.  In a padded batch
     (rows behind the last request, slot -1) the padding's rows of the output
-    are finite where its rows of x are, and mean nothing."""
+    are finite where its rows of x are, and mean nothing.
 
-    COLUMNS = 16  # activation columns of one product call
+    From matmul_from tokens on (None: never) a product is one bq_matmul instead
+    of a call for every 16 tokens: the same numbers to f32 sums, where the
+    calls give the same bits however many tokens there are."""
+
+    COLUMNS = _Products.COLUMNS  # activation columns of one product call
 
     def __init__(self, fmt: int, canon, hidden: int, q_heads: int, cache, norm, freq, max_tokens: int, qa: int = 128,
-                 q_norm=None, k_norm=None, adapters=None, eps: float = 1e-6):
+                 q_norm=None, k_norm=None, adapters=None, eps: float = 1e-6, matmul_from: int | None = None):
         """canon: {"q", "k", "v", "o"} canonical matrices ([q_heads * dim or
         heads * dim, hidden] and [hidden, q_heads * dim]); cache: KVCache;
         norm: float32 [hidden]; adapters: {"q" / "k" / "v" / "o": Adapters}.
@@ -251,13 +285,10 @@ class StagedAttention:
         # the attention leaves rows behind the last request as they were, and the quantizer takes finite values
         self.o.zero_()
         self.o_act, self.o_d, self.out = rows(nq, torch.int8), rows(nq // qa), rows(hidden)
+        self.products = _Products(fmt, self.weights.values(), qa, max_tokens, matmul_from, self.device)
 
     def _product(self, name: str, act, d, y, tokens: int, stream):
-        w = self.weights[name]
-        call = bq_q1_0_matvec if self.fmt == BQ_Q1_0 else bq_q2_0_matvec
-        for c in range(0, tokens, self.COLUMNS):
-            e = min(tokens, c + self.COLUMNS)
-            call(w, Act(act[c:e], d[c:e], w.cols, self.qa, e - c), y[c:e], stream)
+        self.products(self.weights[name], act, d, y, tokens, stream)
 
     def run(self, x, res, pos, slot, cu, lens, table, max_new: int, max_keys: int, ids=None, work=None,
             adapter_work=None, stream=None):
@@ -291,3 +322,109 @@ class StagedAttention:
         if "o" in self.adapters:
             bq_adapters_add(self.adapters["o"], o, cu, ids, max_new, out, work=adapter_work, stream=stream)
         return out, h
+
+
+# --------------------------------------------------------------------- mlp
+class StagedMLP:
+    """The gated MLP of a decoder layer: residual addition, norm and 8-bit
+    activation; gate and up products; activation, gate and 8-bit activation;
+    down product.  Buffers and graphs as in StagedAttention."""
+
+    def __init__(self, fmt: int, canon, hidden: int, inner: int, norm, max_tokens: int, act: int = BQ_SILU, qa: int = 128,
+                 eps: float = 1e-6, matmul_from: int | None = 17, device="cuda"):
+        """canon: {"gate", "up", "down"} canonical matrices ([inner, hidden]
+        twice, [hidden, inner]); norm: float32 [hidden] on the device."""
+        import torch
+
+        self.device = torch.device(device)
+        self.act_kind, self.qa, self.eps, self.norm = act, qa, eps, norm
+        self.weights = {}
+        for name, rows, cols in (("gate", inner, hidden), ("up", inner, hidden), ("down", hidden, inner)):
+            if cols % qa or cols % BLOCK_LEN[fmt]:
+                raise ValueError("every cols must be a multiple of qa and of the block length")
+            self.weights[name] = Weights.upload(fmt, canon[name], rows, cols, device=self.device)
+        self.products = _Products(fmt, self.weights.values(), qa, max_tokens, matmul_from, self.device)
+
+        def rows(n, dtype=torch.float32):
+            return torch.empty(max_tokens, n, dtype=dtype, device=self.device)
+
+        self.h, self.act, self.act_d = rows(hidden), rows(hidden, torch.int8), rows(hidden // qa)
+        self.gate, self.up, self.inner_act, self.inner_d = rows(inner), rows(inner), rows(inner, torch.int8), rows(inner // qa)
+        self.out = rows(hidden)
+
+    def run(self, x, res, stream=None):
+        """x, res: float32 [tokens, hidden], whose sum is the residual stream
+        (res None: x alone).  Returns (x, res) of the next block likewise: the
+        down product and the residual stream in front of it, or, where the
+        product is one bq_matmul, which adds it, their sum and None."""
+        import torch
+
+        T = x.shape[0]
+        h, out, gate, up = (b[:T] for b in (self.h, self.out, self.gate, self.up))
+        with torch.cuda.device(self.device):  # whose stream the products take
+            bq_rmsnorm_q8(x, self.norm, self.eps, self.qa, self.act[:T], self.act_d[:T], res=res, h=h, stream=stream)
+            self.products(self.weights["gate"], self.act, self.act_d, gate, T, stream)
+            self.products(self.weights["up"], self.act, self.act_d, up, T, stream)
+            bq_gated_q8(gate, up, self.act_kind, self.qa, self.inner_act[:T], self.inner_d[:T], stream=stream)
+            wide = self.products.wide(T)
+            self.products(self.weights["down"], self.inner_act, self.inner_d, out, T, stream, res=h if wide else None)
+        return (out, None) if wide else (out, h)
+
+
+# ----------------------------------------------------------------- decoder
+class StagedDecoder:
+    """A decoder from token ids to the next ids: rows of the token table, layers
+    of a StagedAttention and a StagedMLP each, norm and head product of one row
+    a request, and the draw.  A step runs any number of new tokens of any number
+    of requests (prompts, chunks, one token each); its tokens can be the next
+    step's ids where they lie, and a captured step replayed."""
+
+    def __init__(self, table, layers, norm, head, max_tokens: int, max_requests: int, scale: float = 1.0, qa: int = 128,
+                 eps: float = 1e-6, matmul_from: int | None = 17):
+        """table: token table, Weights or a tensor [vocab, hidden]; layers:
+        [(StagedAttention, StagedMLP)]; norm: float32 [hidden]; head: Weights
+        [vocab, hidden] (the table's, where both are the same matrix)."""
+        import torch
+
+        self.table, self.layers, self.norm, self.head = table, list(layers), norm, head
+        self.scale, self.qa, self.eps = scale, qa, eps
+        self.device = norm.device
+        hidden, vocab, B = head.cols, head.rows, max_requests
+
+        def rows(n, count, dtype=torch.float32):
+            return torch.empty(count, n, dtype=dtype, device=self.device)
+
+        self.x = rows(hidden, max_tokens)
+        self.last, self.last_res = rows(hidden, B), rows(hidden, B)
+        self.act, self.act_d = rows(hidden, B, torch.int8), rows(hidden // qa, B)
+        self.logits = rows(vocab, B)
+        self.products = _Products(head.fmt, [head], qa, B, matmul_from, self.device)
+        self.token = torch.empty(B, dtype=torch.int64, device=self.device)
+        self.logprob = torch.empty(B, dtype=torch.float32, device=self.device)
+        need = max(bq_sample_work_bytes(b, vocab) for b in range(1, B + 1))
+        self.sample_work = torch.empty(need, dtype=torch.uint8, device=self.device)
+
+    def run(self, ids, last, u, pos, slot, cu, lens, table, max_new: int, max_keys: int, adapter_ids=None, work=None,
+            adapter_work=None, stream=None, **filters):
+        """ids: int64 [tokens]; last: int64 [requests], the row of each request
+        that its next token follows from; u: float32 [requests]; filters:
+        temperature, top_k, top_p, min_p of bq_sample; the rest as in
+        StagedAttention.run.  Returns (token, logprob) of the requests."""
+        import torch
+
+        T, B = ids.shape[0], last.shape[0]
+        with torch.cuda.device(self.device):  # whose stream the products take
+            x, res = self.x[:T], None
+            bq_embed(self.table, ids, x, scale=self.scale, stream=stream)
+            for attention, mlp in self.layers:
+                x, res = attention.run(x, res, pos, slot, cu, lens, table, max_new, max_keys, ids=adapter_ids, work=work,
+                                       adapter_work=adapter_work, stream=stream)
+                x, res = mlp.run(x, res, stream=stream)
+            bq_embed(x, last, self.last[:B], stream=stream)
+            if res is not None:
+                bq_embed(res, last, self.last_res[:B], stream=stream)
+            bq_rmsnorm_q8(self.last[:B], self.norm, self.eps, self.qa, self.act[:B], self.act_d[:B],
+                          res=None if res is None else self.last_res[:B], stream=stream)
+            self.products(self.head, self.act, self.act_d, self.logits, B, stream)
+            bq_sample(self.logits[:B], u, self.token[:B], logprob=self.logprob[:B], work=self.sample_work, stream=stream, **filters)
+        return self.token[:B], self.logprob[:B]
