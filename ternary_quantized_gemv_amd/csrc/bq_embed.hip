@@ -3,6 +3,10 @@
 // A lane makes eight neighbouring values: of a packed row one byte (Q1_0) or
 // half a word (Q2_0) and the block's scale, of a dense row 16 or 32 bytes.  The
 // pieces of a packed row lie 1 KiB apart (64 rows a tile), 16 bytes each.
+//
+// Measured: 8191 ternary rows of 4096 to bf16 28 us.  That is memory: of every 16-byte
+// piece a line of 128 comes along (75 MB, 17 of them needed), beside 67 MB of outputs
+// (5 TB/s).  Four pieces a lane with their loads under way together: 29.6.  One row 3.2 us.
 #include "bq_device.h"
 #include "bq_half.h"
 #include "bq_model.h"
@@ -53,8 +57,11 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_kernel(const bq_table a)
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 8; ++e) {
                 v[e] *= a.scale;
+                // rounded to f32 before it is narrowed: seen together, the two become one instruction that rounds once
+                asm("" : "+v"(v[e]));
+            }
         }
         store8(static_cast<OUT *>(a.out) + t * a.ld_out + 8 * (int64_t)c, v);
     }

@@ -66,6 +66,14 @@ def _planes(fn: str, w: Weights) -> tuple:
     return (w.fmt, 0, w.rows, w.cols, w.bits.data_ptr(), w.scales.data_ptr()), dev
 
 
+def _work_of(fn: str, work, need: int, dev: int, stream) -> tuple:
+    """Pointer and bytes of the scratch, and what keeps it: the caller's, one of this call, or none."""
+    if work is None and not need:
+        return 0, 0, None
+    work = _scratch(fn, work, need, dev, stream)
+    return work.data_ptr(), work.nbytes, work
+
+
 def bq_embed(table, ids, out, scale: float = 1.0, stream=None) -> None:
     """out[t] = scale * table[ids[t]].  table: Weights, or a tensor [count, n]
     (float32, float16 or bfloat16); ids: int64 [tokens] (-1: a row of zeros);
@@ -131,13 +139,12 @@ def bq_matmul(w: Weights, a: Act, y, bias=None, act: int = BQ_NONE, mul=None, re
     shape = (T, w.rows)
     yp = _rows(fn, "y", y, dt, dev, shape)
     need = _matmul_work(w.fmt, w.rows, w.cols, a.qa, T, kind)
-    work = _scratch(fn, work, need, dev, stream)
+    wp, size, keep = _work_of(fn, work, need, dev, stream)
     ld_q, ld_d = a._ld()
     p = _pack_product(*planes, a.q.data_ptr(), a.d.data_ptr(), a.n, a.qa, T, ld_q, ld_d, kind, act,
                       0 if bias is None else _flat(fn, "bias", bias, torch.float32, dev, w.rows),
                       *((0, 0) if mul is None else _rows(fn, "mul", mul, dt, dev, shape)),
-                      *((0, 0) if res is None else _rows(fn, "res", res, dt, dev, shape)), *yp, work.data_ptr(),
-                      work.nbytes)
+                      *((0, 0) if res is None else _rows(fn, "res", res, dt, dev, shape)), *yp, wp, size)
     _run(lib.bq_matmul, p, dev, stream)
 
 
@@ -171,10 +178,10 @@ def bq_sample(logits, u, token, logprob=None, temperature=None, top_k=None, top_
 
     if u is None or token is None:
         _refuse(fn, "u and token must be tensors")
-    work = _scratch(fn, work, _sample_work(kind, B, V), dev, stream)
+    wp, size, keep = _work_of(fn, work, _sample_work(kind, B, V), dev, stream)
     a = _pack_draw(kind, 0, B, V, *p, each("u", u), each("temperature", temperature), each("top_k", top_k, torch.int32),
                    each("top_p", top_p), each("min_p", min_p), each("token", token, torch.int64), each("logprob", logprob),
-                   work.data_ptr(), work.nbytes)
+                   wp, size)
     _run(lib.bq_sample, a, dev, stream)
 
 
