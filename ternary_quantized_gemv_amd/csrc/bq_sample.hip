@@ -39,7 +39,7 @@ struct Scale {
     double top;     // the largest logit
     double per;     // 32 log2(e) / T
     float topf;
-    float buckets;  // a unit of logit
+    float buckets;  // two units of logit
     int bits;       // weights are multiples of 2^-bits
     bool greedy;
 };
@@ -55,7 +55,7 @@ __device__ __forceinline__ Scale scale_of_row(uint32_t top, float t, int vocab)
     s.bits = 62 - wide < 50 ? 62 - wide : 50;
     // kBuckets of them hold bits + 2 halvings: behind the last one every weight rounds to 0 (bits + 1 would do; f32
     // is off by far less than that)
-    s.buckets = (float)(kBuckets / 32.0 * s.per / (double)(s.bits + 2));
+    s.buckets = (float)(kBuckets / 16.0 * s.per / (double)(s.bits + 2));
     return s;
 }
 
@@ -64,7 +64,8 @@ __device__ __forceinline__ int bucket_of(const Scale &s, float l)
 {
     if (l == s.topf)
         return 0;
-    const float x = (s.topf - l) * s.buckets;
+    // half the difference: the whole one may be past f32's range
+    const float x = __builtin_fmaf(l, -0.5f, 0.5f * s.topf) * s.buckets;
     return !s.greedy && x < (float)kBuckets ? (int)x : kBuckets;
 }
 // Every logit of buckets 0 .. b is at least this (the slack is far above what bucket_of's roundings come to; a NaN, from
@@ -73,7 +74,7 @@ __device__ __forceinline__ float least_logit(const Scale &s, int b)
 {
     if (s.greedy)
         return s.topf;
-    return s.topf - (float)(b + 1) / s.buckets * 1.0001f - fabsf(s.topf) * 0x1p-20f;
+    return s.topf - (float)(2 * b + 2) / s.buckets * 1.0001f - fabsf(s.topf) * 0x1p-20f;
 }
 // exp((l - top) / T) in units of 2^-bits, before it is rounded: 2^(y / 32) with y = n + f, |f| <= 1/2, of which 2^(f / 32)
 // is exp(f ln 2 / 32) by its series (the first term left out is below 2^-48 of it), and 2^(n % 32 / 32) from a table.
@@ -469,7 +470,7 @@ __device__ void pick(Room &r, const bq_draw &a, const Scale &s, const T *row, in
     auto share_of = [&](u64 mass) {
         const double want = share * (double)mass;
         const u64 target = want > 0.0 ? (u64)__builtin_ceil(want) : 1;
-        return target < 1 ? 1 : target > mass ? mass : target;
+        return target > mass && mass ? mass : target < 1 ? 1 : target;
     };
     const double u = s.greedy ? 0.0 : (double)a.u[at];
     auto drawn_of = [&](u64 mass) {

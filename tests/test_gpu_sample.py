@@ -148,6 +148,21 @@ def test_rows_without_weight_and_non_finite(dt):
     assert np.isclose(logprob[4], -np.log(677), rtol=1e-6) and logprob[5] == 0
 
 
+def test_differences_past_the_range_of_f32():
+    """Logits at both ends of f32 under a temperature that brings them near each other."""
+    t = torch()
+    x = t.full((4, 900), -3e38)
+    x[:, 5], x[:, 700] = 3e38, 0.0
+    temp = np.float32(1e38)
+    w = np.exp(np.array([0.0, -3.0, -6.0]))  # of 5, 700 and the others
+    total = w[0] + w[1] + 898 * w[2]
+    at = [w[0] / 2, w[0] + w[1] / 2, w[0] + w[1] + 0.5 * w[2], w[0] + w[1] + 897.5 * w[2]]
+    token, logprob = run(x.cuda(), np.array(at) / total, temperature=[temp] * 4, top_p=[1.0, 1.0, 0.999, 1.0])
+    assert token.tolist()[:2] == [5, 700] and token[2] == 0 and token[3] == 899
+    want = np.log(np.array([w[0], w[1], w[2], w[2]]) / total)
+    assert np.allclose(logprob, want, rtol=0, atol=6 * 2.0 ** -22)  # T and the logits are f32: 6 nats off by two roundings
+
+
 def test_signed_zeros_are_one_value():
     t = torch()
     x = t.zeros(1, 4000)
