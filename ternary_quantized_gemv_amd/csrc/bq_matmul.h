@@ -235,6 +235,7 @@ __device__ __forceinline__ void store_rows(const bq_product &a, float (&x)[N], c
         if (live[e])
             static_cast<T *>(a.y)[t[e] * a.ld_y + r] = (T)x[e];
 }
+// (v_rcp_f32 is good to one unit in the last place; of an infinity it is 0.)
 template <int N>
 __device__ __forceinline__ void finish(const bq_product &a, float (&x)[N], const int64_t (&t)[N], const bool (&live)[N], int64_t r)
 {
@@ -248,12 +249,12 @@ __device__ __forceinline__ void finish(const bq_product &a, float (&x)[N], const
     case BQ_SILU:
 #pragma unroll
         for (int e = 0; e < N; ++e)
-            x[e] = x[e] / (1.0f + expf(-x[e]));
+            x[e] *= __builtin_amdgcn_rcpf(1.0f + expf(-x[e]));
         break;
     case BQ_GELU:
 #pragma unroll
         for (int e = 0; e < N; ++e)
-            x[e] = x[e] / (1.0f + expf(-1.59576912160573f * __builtin_fmaf(0.044715f * x[e] * x[e], x[e], x[e])));
+            x[e] *= __builtin_amdgcn_rcpf(1.0f + expf(-1.59576912160573f * __builtin_fmaf(0.044715f * x[e] * x[e], x[e], x[e])));
         break;
     case BQ_RELU2:
 #pragma unroll
