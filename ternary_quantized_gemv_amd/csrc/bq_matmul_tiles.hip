@@ -13,7 +13,8 @@
 // cores' 5 PFLOP/s.  4096 x 4096 x 4096 in Q1_0 takes 118 us (1170 TFLOP/s), of which 9
 // are the layout and about 24 the outputs (67 MB at 2.8 TB/s); 12288 columns in Q2_0
 // 378 us (1090).  128 tokens a workgroup spill registers (114 and 380 us), as do three
-// wavefronts a SIMD (122 and 840); orders of the instructions by hand, priorities around
+// wavefronts a SIMD (122 and 840); outputs from the products' own places, 128 bytes a
+// token, took 47 us instead of 30; orders of the instructions by hand, priorities around
 // the matrix instructions and starting values kept in registers changed nothing.
 #include "bq_matmul.h"
 
@@ -176,9 +177,8 @@ __global__ __launch_bounds__(256 * KG, 2) void matmul_tiles(const MatmulArgs g)
                 }
             }
         }
-        // through LDS, 32 tokens at a time, to 64 rows side by side (256 bytes a store; from the products' own
-        // places, 128 bytes a token, 67 MB took 47 us instead of 30): column c of token t at c ^ 32 (t / 4 % 2), so
-        // that the lane halves, 4 tokens apart, write to different banks.  The groups of wavefronts add up there.
+        // through LDS, 32 tokens at a time, to 64 rows side by side: column c of token t at c ^ 32 (t / 4 % 2), so that
+        // the lane halves, 4 tokens apart, write to different banks.  The groups of wavefronts add up there.
         float *out = reinterpret_cast<float *>(lds) + wave * 2048;
         const int64_t r = want * 64 + lane;
 #pragma unroll

@@ -8,8 +8,14 @@
 // end at a place of it: each is "the first token at which the running sum (of
 // weights, or of ones) reaches a target".  One pass finds the row's largest
 // logit; one more counts tokens and weights in 1024 buckets of (m - l) / T, whose
-// running sums say in which bucket a target is reached; only that bucket's tokens
-// are then looked at, ordered by (logit, -index).
+// running sums say in which bucket a target is reached; a third collects the tokens of
+// the few buckets that the filters and the draw can need, ordered by (logit, -index).
+//
+// Up to 256 rows the first two passes are launches over slices of the rows, sixteen at
+// most; the third is one workgroup a row (with more rows, all three are).  Measured: one
+// row of 151936 f32 32 us (4.6, 7.2 and 20 in the kernels: one workgroup reads 600 KB),
+// 192 rows 126 us (22, 52, 57: 117 MB three times at up to 5.4 TB/s; the middle one is
+// bound by its weights in binary64 and by LDS atomics), 33 rows of 32001 bf16 35 us.
 #include "bq_half.h"
 #include "bq_model.h"
 
