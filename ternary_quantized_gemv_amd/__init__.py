@@ -11,6 +11,7 @@ this package fails if the library has not been built
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -237,12 +238,15 @@ def bq_read_floor(buf, sink, stream=None) -> None:
                              _stream(stream)))
 
 
+_plane_sizes = functools.lru_cache(maxsize=1024)(bq_packed_bytes)  # of one shape always the same
+
+
 class Weights:
     """A packed matrix resident on the GPU (the two planes of bq_pack)."""
 
     def __init__(self, fmt: int, rows: int, cols: int, bits, scales):
         import torch
-        nb, ns = bq_packed_bytes(fmt, rows, cols)
+        nb, ns = _plane_sizes(fmt, rows, cols)
         _need(bits, "weights.bits", torch.uint8, nb, "Weights")
         _need(scales, "weights.scales", torch.int16, ns // 2, "Weights")
         self.fmt, self.rows, self.cols = fmt, rows, cols
