@@ -202,7 +202,7 @@ def test_streams_scratch_and_graphs(T, rows):
 
 
 def test_large_offsets():
-    """Outputs past 2^31 and 2^32 bytes: 151936 rows of 8 tokens more than 2^32 / (4 rows)."""
+    """Outputs whose byte offsets pass 2^31 and 2^32: 40000 rows of 30001 tokens."""
     t, bq = torch(), bqmod()
     rows, T = 40000, 30001  # 4.8 GB of f32
     canon = synth.q1_0_blocks(rows, 128, 1)
