@@ -235,7 +235,14 @@ __device__ __forceinline__ void store_rows(const bq_product &a, float (&x)[N], c
         if (live[e])
             static_cast<T *>(a.y)[t[e] * a.ld_y + r] = (T)x[e];
 }
-// (v_rcp_f32 is good to one unit in the last place; of an infinity it is 0.)
+// x / (1 + exp(-z)) for a z of x's sign, from exp(-|z|): the sum is 1 to 2, where v_rcp_f32 is good to one unit in the
+// last place, and far below zero x exp(z) stays (1 + exp(-z) has a reciprocal of 0 from 2^126 on, its inverse being
+// subnormal: z below -87.3, where the result is down to -1e-36).
+__device__ __forceinline__ float sigmoid_times(float x, float z)
+{
+    const float e = expf(-fabsf(z));
+    return (x < 0.0f ? x * e : x) * __builtin_amdgcn_rcpf(1.0f + e);
+}
 template <int N>
 __device__ __forceinline__ void finish(const bq_product &a, float (&x)[N], const int64_t (&t)[N], const bool (&live)[N], int64_t r)
 {
@@ -249,12 +256,12 @@ __device__ __forceinline__ void finish(const bq_product &a, float (&x)[N], const
     case BQ_SILU:
 #pragma unroll
         for (int e = 0; e < N; ++e)
-            x[e] *= __builtin_amdgcn_rcpf(1.0f + expf(-x[e]));
+            x[e] = sigmoid_times(x[e], x[e]);
         break;
     case BQ_GELU:
 #pragma unroll
         for (int e = 0; e < N; ++e)
-            x[e] *= __builtin_amdgcn_rcpf(1.0f + expf(-1.59576912160573f * __builtin_fmaf(0.044715f * x[e] * x[e], x[e], x[e])));
+            x[e] = sigmoid_times(x[e], 1.59576912160573f * __builtin_fmaf(0.044715f * x[e] * x[e], x[e], x[e]));
         break;
     case BQ_RELU2:
 #pragma unroll
