@@ -45,7 +45,9 @@ struct Scale {
     double top;     // the largest logit
     double per;     // 32 log2(e) / T
     float topf;
-    float buckets;  // two units of logit
+    float unit;     // of a difference of logits, for bucket_of: half, or 2^100 where T is tiny
+    float back;     // 1 / unit
+    float buckets;  // a unit
     int bits;       // weights are multiples of 2^-bits
     bool greedy;
 };
@@ -60,8 +62,11 @@ __device__ __forceinline__ Scale scale_of_row(uint32_t top, float t, int vocab)
     const int wide = 32 - __builtin_clz((unsigned)vocab);
     s.bits = 62 - wide < 50 ? 62 - wide : 50;
     // kBuckets of them hold bits + 2 halvings: behind the last one every weight rounds to 0 (bits + 1 would do; f32
-    // is off by far less than that)
-    s.buckets = (float)(kBuckets / 16.0 * s.per / (double)(s.bits + 2));
+    // is off by far less than that).  Half a difference: the whole one may be past f32's range.  2^100 of it under a T
+    // whose buckets a unit would be: where that overflows the difference is 2^27 of T and more.
+    s.unit = t < 0x1p-100f ? 0x1p100f : 0.5f;
+    s.back = t < 0x1p-100f ? 0x1p-100f : 2.0f;
+    s.buckets = (float)(kBuckets / 32.0 * s.per * (double)s.back / (double)(s.bits + 2));
     return s;
 }
 
@@ -70,8 +75,7 @@ __device__ __forceinline__ int bucket_of(const Scale &s, float l)
 {
     if (l == s.topf)
         return 0;
-    // half the difference: the whole one may be past f32's range
-    const float x = __builtin_fmaf(l, -0.5f, 0.5f * s.topf) * s.buckets;
+    const float x = __builtin_fmaf(l, -s.unit, s.unit * s.topf) * s.buckets;
     return !s.greedy && x < (float)kBuckets ? (int)x : kBuckets;
 }
 // Every logit of buckets 0 .. b is at least this (the slack is far above what bucket_of's roundings come to; a NaN, from
@@ -80,7 +84,7 @@ __device__ __forceinline__ float least_logit(const Scale &s, int b)
 {
     if (s.greedy)
         return s.topf;
-    return s.topf - (float)(2 * b + 2) / s.buckets * 1.0001f - fabsf(s.topf) * 0x1p-20f;
+    return s.topf - (float)(b + 1) * s.back / s.buckets * 1.0001f - fabsf(s.topf) * 0x1p-20f;
 }
 // exp((l - top) / T) in units of 2^-bits, before it is rounded: 2^(y / 32) with y = n + f, |f| <= 1/2, of which 2^(f / 32)
 // is exp(f ln 2 / 32) by its series (the first term left out is below 2^-48 of it), and 2^(n % 32 / 32) from a table.
