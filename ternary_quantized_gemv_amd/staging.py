@@ -337,6 +337,8 @@ class StagedMLP:
         import torch
 
         self.device = torch.device(device)
+        if self.device.index is None:  # the current one now, whichever is current when it runs
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self.act_kind, self.qa, self.eps, self.norm = act, qa, eps, norm
         self.weights = {}
         for name, rows, cols in (("gate", inner, hidden), ("up", inner, hidden), ("down", hidden, inner)):
