@@ -177,16 +177,19 @@ static hipError_t launch_matmul_split(MatmulArgs g, hipStream_t st)
 //   256         25     25    42       4096          328  132  118
 //   Q2_0: 256 tokens 32, 33, 65; 96 tokens of 12288 rows 39, 32, 61; 4096 tokens of 12288 columns 1261, 590, 378
 //   Q1_0 in groups of 32: 256 tokens 51, 37, 76; 1000 tokens of 5000 rows 236, 99, 87
+//   151936 rows: 17 tokens 78, 52, 85 (Q2_0 118, 89, 121); 32 tokens 104, 51, 82 (141, 91, 122); 48 tokens 164, 74, 84
+//   (241, 144, 123)
 // A tile kernel needs its workgroups to fill the 256 compute units: below 128 of 32 tokens (1024 of the split kernel's)
 // the split kernel, whose wavefronts share out the steps, is faster; it lays the tokens out anew for every 32 rows,
-// which costs more with short groups.  64 tokens decode the weights half as often, and pay from a second workgroup a
-// compute unit on.
+// which costs more with short groups.
+// 64 tokens decode the weights half as often, and pay from a second workgroup a compute unit on; not with 32 tokens or
+// fewer, which are one tile either way, half of it empty.
 static int kernel_for(const bq_product &a)
 {
     const int64_t t = a.a.ncols, r = a.w.rows;
     if (up(t, 32) * up(r, 32) <= (a.a.qa < block_len(a.w.fmt) ? 640 : 1024))
         return 0;
-    return up(t, 64) * up(r, kTileOut) <= 256 ? 32 : 64;
+    return t <= 32 || up(t, 64) * up(r, kTileOut) <= 256 ? 32 : 64;
 }
 
 int64_t matmul_work(const bq_product &a)
