@@ -179,15 +179,18 @@ static hipError_t launch_matmul_split(MatmulArgs g, hipStream_t st)
 //   Q1_0 in groups of 32: 256 tokens 51, 37, 76; 1000 tokens of 5000 rows 236, 99, 87
 //   151936 rows: 17 tokens 78, 52, 85 (Q2_0 118, 89, 121); 32 tokens 104, 51, 82 (141, 91, 122); 48 tokens 164, 74, 84
 //   (241, 144, 123)
+//   20000 tokens: 40 rows 36, 74, 76 (Q2_0 42, 110, 98); 128 rows 58, 74, 77 (74, 112, 99); 200 rows 100, 74, 78
+//   (127, 112, 100).  100000 tokens of 256 columns in groups of 32, Q2_0: 40 rows 44, 98, 64; 128 rows 83, 99, 65
 // A tile kernel needs its workgroups to fill the 256 compute units: below 128 of 32 tokens (1024 of the split kernel's)
 // the split kernel, whose wavefronts share out the steps, is faster; it lays the tokens out anew for every 32 rows,
-// which costs more with short groups.
+// which costs more with short groups.  So it is with up to 64 rows, where three of a tile's four wavefronts would work
+// for nothing.
 // 64 tokens decode the weights half as often, and pay from a second workgroup a compute unit on; not with 32 tokens or
 // fewer, which are one tile either way, half of it empty.
 static int kernel_for(const bq_product &a)
 {
     const int64_t t = a.a.ncols, r = a.w.rows;
-    if (up(t, 32) * up(r, 32) <= (a.a.qa < block_len(a.w.fmt) ? 640 : 1024))
+    if (r <= kTileRows || up(t, 32) * up(r, 32) <= (a.a.qa < block_len(a.w.fmt) ? 640 : 1024))
         return 0;
     return t <= 32 || up(t, 64) * up(r, kTileOut) <= 256 ? 32 : 64;
 }

@@ -1,5 +1,5 @@
 """bq_matmul at the ends of its range of shapes: a head of many rows for a handful
-of tokens."""
+of tokens, a projection to few rows of many tokens."""
 import numpy as np
 import pytest
 
@@ -20,6 +20,16 @@ def test_many_rows_few_tokens(fmt, qa, cols, T):
     q, d = acts(T, cols, qa, T)
     y = run(bq.Weights.upload(fmt, canon, rows, cols), q, d, qa, torch().float32)
     within(y, *matmul_ref(fmt, canon, q, d, qa, torch().float32), (fmt, qa, T))
+
+
+@pytest.mark.parametrize("fmt,qa,cols", [(1, 128, 256), (1, 32, 128), (2, 64, 320), (2, 128, 128)])
+@pytest.mark.parametrize("rows", [1, 40, 64, 65])
+def test_few_rows_many_tokens(fmt, qa, cols, rows):
+    bq, T = bqmod(), 20001
+    canon = synth.blocks(fmt, rows, cols, 3, rows)
+    q, d = acts(T, cols, qa, rows)
+    y = run(bq.Weights.upload(fmt, canon, rows, cols), q, d, qa, torch().float32)
+    within(y, *matmul_ref(fmt, canon, q, d, qa, torch().float32), (fmt, qa, rows))
 
 
 def test_head_of_a_batch():
