@@ -570,8 +570,9 @@ int bq_adapters_work_bytes(const bq_adapters *a, int64_t *bytes);
  * apart (w.bits, w.scales NULL; dense NULL where w.fmt is not 0).  A token
  * whose id is not in [0, w.rows) (-1: padding) gets a row of zeros.  ids is
  * an int64 device array.  Dense rows and rows of out are 16-byte aligned
- * (leading dimensions multiples of 16 bytes), w.cols a multiple of 8, and of
- * the block length where the table is packed, below 2^31.  scale is finite.
+ * (leading dimensions multiples of 16 bytes), w.cols a multiple of 8 below
+ * 2^31, and of a packed table as in bq_pack: a multiple of the block length,
+ * at most 268,435,328 (Q1_0) or 134,217,664 (Q2_0).  scale is finite.
  * out must not overlap the table or ids.  tokens = 0 does nothing.  Returns
  * BQ_EARG / BQ_EALIGN before any launch, or BQ_EHIP.  Allocates nothing.
  * Asynchronous on s. */
@@ -637,7 +638,7 @@ int bq_gated_q8(const bq_gated *a, bq_stream s);
  * otherwise overlap an input.  Scales and results are finite.
  * a.q, w's planes and work are 16-byte aligned (a.ld_q a multiple of 16); the
  * other arrays by their elements, with any leading dimension of at least
- * w.rows.  w.cols is below 2^31.
+ * w.rows.  w.cols is at most 268,435,328 (Q1_0) or 134,217,664 (Q2_0).
  * work (bq_matmul_work_bytes bytes; may be NULL if that is 0) is scratch of
  * this call until it has run: calls that may run at the same time need one
  * each.  a.ncols = 0 does nothing.  Returns BQ_EARG / BQ_EALIGN before any

@@ -52,6 +52,9 @@ int check_product(const char *fn, const bq_product *a)
     if (a->w.cols % block_len(a->w.fmt) || a->w.cols % a->a.qa)
         return set_error(BQ_EARG, "%s: cols %lld not a multiple of %d and of qa %d", fn, (long long)a->w.cols,
                          block_len(a->w.fmt), (int)a->a.qa);
+    if (!tile_fits(a->w.cols / block_len(a->w.fmt)))
+        return set_error(BQ_EARG, "%s: cols %lld: a 64-row tile's payload would exceed %lld bytes", fn,
+                         (long long)a->w.cols, (long long)kMaxTileBytes);
     return BQ_OK;
 }
 
