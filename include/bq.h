@@ -596,8 +596,9 @@ int bq_embed(const bq_table *a, bq_stream s);
  *   v = act(gate) * up, evaluated in binary64 and rounded once to f32
  *   d, q as bq_rmsnorm_q8 forms them from v (blocks of qa, f16_scale)
  *   y = v rounded to `type`
- * so q and d do not hang on how exp is computed (but for a v within 2^-50 of
- * where it rounds the other way).  gate, up and y hold `type`, rows ld_*
+ * so q and d do not hang on how exp is computed, but for a v that lies within
+ * 2^-50 of its size (BQ_GELU: within (1 + 2 |z|) 2^-50, z as above at the gate,
+ * whose rounding exp magnifies) of where it rounds the other way.  gate, up and y hold `type`, rows ld_*
  * elements apart; y may be NULL, gate or up (same leading dimension), and not
  * otherwise overlap them.  n is a multiple of qa below 2^31, qa 32, 64 or
  * 128.  gate, up and y rows are 16-byte aligned, q 8-byte with ld_q a
