@@ -235,13 +235,28 @@ __device__ __forceinline__ void store_rows(const bq_product &a, float (&x)[N], c
         if (live[e])
             static_cast<T *>(a.y)[t[e] * a.ld_y + r] = (T)x[e];
 }
-// x / (1 + exp(-z)) for a z of x's sign, from exp(-|z|): the sum is 1 to 2, where v_rcp_f32 is good to one unit in the
-// last place, and far below zero x exp(z) stays (1 + exp(-z) has a reciprocal of 0 from 2^126 on, its inverse being
-// subnormal: z below -87.3, where the result is down to -1e-36).
-__device__ __forceinline__ float sigmoid_times(float x, float z)
+// x / (1 + exp(-z)) with z = z_of(x), which has x's sign and rises with x.  v_rcp_f32 is good to one unit in the last
+// place, but gives 0 where the inverse is subnormal, from 1 + exp(-z) = 2^126 (z below -87.3) on; the result is down to
+// -1e-36 there.  With exp(-|z|) the sum is 1 to 2: for all N of a lane if one is that far below zero (2049 x 12288 x 4096
+// 202 us with this form alone, 200 with both).
+template <int N, class Z>
+__device__ __forceinline__ void times_sigmoid(float (&x)[N], Z z_of)
 {
-    const float e = expf(-fabsf(z));
-    return (x < 0.0f ? x * e : x) * __builtin_amdgcn_rcpf(1.0f + e);
+    float low = x[0];
+#pragma unroll
+    for (int e = 1; e < N; ++e)
+        low = fminf(low, x[e]);
+    if (z_of(low) > -80.0f) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            x[e] *= __builtin_amdgcn_rcpf(1.0f + expf(-z_of(x[e])));
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const float y = expf(-fabsf(z_of(x[e])));
+        x[e] = (x[e] < 0.0f ? x[e] * y : x[e]) * __builtin_amdgcn_rcpf(1.0f + y);
+    }
 }
 template <int N>
 __device__ __forceinline__ void finish(const bq_product &a, float (&x)[N], const int64_t (&t)[N], const bool (&live)[N], int64_t r)
@@ -253,15 +268,9 @@ __device__ __forceinline__ void finish(const bq_product &a, float (&x)[N], const
             x[e] += b;
     }
     switch (a.act) {
-    case BQ_SILU:
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            x[e] = sigmoid_times(x[e], x[e]);
-        break;
+    case BQ_SILU: times_sigmoid<N>(x, [](float v) { return v; }); break;
     case BQ_GELU:
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            x[e] = sigmoid_times(x[e], 1.59576912160573f * __builtin_fmaf(0.044715f * x[e] * x[e], x[e], x[e]));
+        times_sigmoid<N>(x, [](float v) { return 1.59576912160573f * __builtin_fmaf(0.044715f * v * v, v, v); });
         break;
     case BQ_RELU2:
 #pragma unroll
