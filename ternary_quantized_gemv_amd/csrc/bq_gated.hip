@@ -8,9 +8,9 @@
 // six roundings more, 2^-53 each, which move exp by 2 |z| times as much.  Eight values a lane, a block of
 // qa in qa / 8 neighbouring lanes, quantized as the norm does (bq_quant8.h).
 //
-// Measured: 4099 x 12288 bf16 with the values kept (359 MB) 118 us, 3.0 TB/s: about 30
+// Measured: 4099 x 12288 bf16 with the values kept (359 MB) 121 us, 3.0 TB/s: about 30
 // operations of binary64 a value beside the memory's 76 us at the rate of a copy (the
-// next piece's loads under way meanwhile: 126).  16 x 12288 f32 4.2 us, latency.
+// next piece's loads under way meanwhile: 126).  16 x 12288 f32 4.4 us, latency.
 #include "bq_half.h"
 #include "bq_model.h"
 #include "bq_quant8.h"

@@ -7,15 +7,17 @@
 // ahead.  KG groups of four wavefronts take every KG-th step, for few tiles.
 //
 // What bounds it: 32 tokens x 32 rows x 128 k are four matrix instructions of 32 cycles
-// and 32 fma (Q2_0: 64) beside about 12 other operations.  Two wavefronts a SIMD, a
-// matrix instruction keeps the vector unit for about 15 of its 32 cycles (measured with
-// both in a loop), so the two add up: 4 x 15 + 44 x 3.7 = 220 cycles, 2.4 of the matrix
-// cores' 5 PFLOP/s.  4096 x 4096 x 4096 in Q1_0 takes 118 us (1170 TFLOP/s), of which 9
-// are the layout and about 24 the outputs (67 MB at 2.8 TB/s); 12288 columns in Q2_0
-// 378 us (1090).  128 tokens a workgroup spill registers (114 and 380 us), as do three
-// wavefronts a SIMD (122 and 840); outputs from the products' own places, 128 bytes a
-// token, took 47 us instead of 30; orders of the instructions by hand, priorities around
-// the matrix instructions and starting values kept in registers changed nothing.
+// and 32 scaling fma (Q2_0: 64).  The counters at 4096 x 4096 x 4096 in Q1_0 say 63 vector
+// and matrix instructions for each such unit (16 decode the weights, the others are
+// addresses and the outputs) and 467 cycles of a SIMD (239 K for 512 units): its vector
+// unit is busy for 54% of them, its matrix cores for 27%, mostly in turn (two wavefronts a
+// SIMD, a matrix instruction keeps the vector unit for about 15 of its 32 cycles: measured
+// with both in a loop); the rest is waiting.  118 us (1170 TFLOP/s of the matrix cores'
+// 5000), of which 9 are the layout and about 24 the outputs (67 MB at 2.8 TB/s); 12288
+// columns in Q2_0 380 us (1085).  128 tokens a workgroup spill registers (114 and 380 us),
+// as do three wavefronts a SIMD (122 and 840); outputs from the products' own places, 128
+// bytes a token, took 47 us instead of 30; orders of the instructions by hand, priorities
+// around the matrix instructions and starting values kept in registers changed nothing.
 #include "bq_matmul.h"
 
 namespace bq {

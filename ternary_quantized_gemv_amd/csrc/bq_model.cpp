@@ -13,7 +13,7 @@ using namespace bq;
 
 namespace {
 
-// a tile of tokens past the last one is still counted in 32 bits
+// a.ncols is an int32; some tiles of tokens below its end
 constexpr int64_t kMatmulTokens = kRowsMax - (1 << 16);
 
 bool known_act(int act) { return act == BQ_NONE || act == BQ_SILU || act == BQ_GELU || act == BQ_RELU2; }

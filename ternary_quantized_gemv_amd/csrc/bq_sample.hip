@@ -13,8 +13,8 @@
 //
 // Up to 256 rows the first two passes are launches over slices of the rows, sixteen at
 // most; the third is one workgroup a row (with more rows, all three are).  Measured: one
-// row of 151936 f32 32 us (4.6, 7.2 and 20 in the kernels: one workgroup reads 600 KB),
-// 192 rows 126 us (22, 52, 57: 117 MB three times at up to 5.4 TB/s; the middle one is
+// row of 151936 f32 27 to 44 us by the filters' places (4.6, 7.3 and 22 in the kernels: one workgroup reads 600 KB),
+// 192 rows 128 us (21, 53, 58: 117 MB three times at up to 5.4 TB/s; the middle one is
 // bound by its weights in binary64 and by LDS atomics), 33 rows of 32001 bf16 35 us.
 #include "bq_half.h"
 #include "bq_model.h"

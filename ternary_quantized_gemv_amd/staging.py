@@ -379,7 +379,13 @@ class StagedDecoder:
     of a StagedAttention and a StagedMLP each, norm and head product of one row
     a request, and the draw.  A step runs any number of new tokens of any number
     of requests (prompts, chunks, one token each); its tokens can be the next
-    step's ids where they lie, and a captured step replayed."""
+    step's ids where they lie, and a captured step replayed.  Buffers as in
+    StagedAttention: steps on two streams at once need two objects, layers
+    included, and the next step writes the returned tokens again.
+
+    matmul_from here is of the head alone.  The layers have their own: 17 in
+    StagedMLP, but None in StagedAttention, whose q, k, v and o products then
+    take a prompt 16 tokens at a time; give it one for long prompts."""
 
     def __init__(self, table, layers, norm, head, max_tokens: int, max_requests: int, scale: float = 1.0, qa: int = 128,
                  eps: float = 1e-6, matmul_from: int | None = 17):
