@@ -63,9 +63,11 @@ __device__ __forceinline__ Scale scale_of_row(uint32_t top, float t, int vocab)
     s.bits = 62 - wide < 50 ? 62 - wide : 50;
     // kBuckets of them hold bits + 2 halvings: behind the last one every weight rounds to 0 (bits + 1 would do; f32
     // is off by far less than that).  Half a difference: the whole one may be past f32's range.  2^100 of it under a T
-    // whose buckets a unit would be: where that overflows the difference is 2^27 of T and more.
-    s.unit = t < 0x1p-100f ? 0x1p100f : 0.5f;
-    s.back = t < 0x1p-100f ? 0x1p-100f : 2.0f;
+    // whose buckets a unit would be; not with a largest logit of 2^27 and more, which so much of would be infinite
+    // (any logit below it is by 8, past the last bucket with infinitely many a unit too).
+    const bool tiny = t < 0x1p-100f && fabsf(s.topf) < 0x1p27f;
+    s.unit = tiny ? 0x1p100f : 0.5f;
+    s.back = tiny ? 0x1p-100f : 2.0f;
     s.buckets = (float)(kBuckets / 32.0 * s.per * (double)s.back / (double)(s.bits + 2));
     return s;
 }

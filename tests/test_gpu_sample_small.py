@@ -34,3 +34,24 @@ def test_tiny_temperatures(vocab, temp, shift):
     share = (r.sums[3] - 0.5 * r.w[3]) / r.sums[-1]
     token, _ = run(t.from_numpy(np.tile(x, (2, 1))).cuda(), [top] * 2, [temp] * 2, top_k=[3, 0], top_p=[1.0, share])
     assert token.tolist() == [r.order[2], r.order[3]]
+
+
+@pytest.mark.parametrize("vocab", [9, 5000, 40000])
+@pytest.mark.parametrize("temp", [2.0 ** -99, 2.0 ** -101, 1e-38, 2.0 ** -149])
+def test_tiny_temperatures_and_large_logits(vocab, temp):
+    """The largest logit far from zero on either side: nothing but its equals weighs anything."""
+    t = torch()
+    g = np.random.default_rng(vocab)
+    tops = [-3.4e38, -1e30, -2.0 ** 28, -2.0 ** 27, -1.0, 1.0, 2.0 ** 27, 2.0 ** 28, 1e30, 3.4e38]
+    x = np.empty((len(tops), vocab), np.float32)
+    for b, top in enumerate(tops):
+        top = np.float32(top)
+        x[b] = np.nextafter(top, np.float32(-np.inf))
+        x[b, g.permutation(vocab)[:vocab // 3]] = -np.inf
+        x[b, g.permutation(vocab)[:2]] = top
+    equal = [np.flatnonzero(row == np.float32(top)) for row, top in zip(x, tops)]
+    rows = t.from_numpy(x).cuda()
+    for u, which in ((0.25, 0), (0.75, 1)):
+        token, logprob = run(rows, [u] * len(tops), [temp] * len(tops))
+        assert token.tolist() == [int(e[which]) for e in equal]
+        assert np.allclose(logprob, -np.log(2.0), rtol=1e-6)
