@@ -598,11 +598,12 @@ int bq_embed(const bq_table *a, bq_stream s);
  *   y = v rounded to `type`
  * so q and d do not hang on how exp is computed, but for a v that lies within
  * 2^-50 of its size (BQ_GELU: within (1 + 2 |z|) 2^-50, z as above at the gate,
- * whose rounding exp magnifies) of where it rounds the other way.  gate, up and y hold `type`, rows ld_*
- * elements apart; y may be NULL, gate or up (same leading dimension), and not
- * otherwise overlap them.  n is a multiple of qa below 2^31, qa 32, 64 or
- * 128.  gate, up and y rows are 16-byte aligned, q 8-byte with ld_q a
- * multiple of 16, d 4-byte.  Values are finite, act(gate) * up too.
+ * whose rounding exp magnifies) of where it rounds the other way.  gate, up
+ * and y hold `type`, rows ld_* elements apart; y may be NULL, gate or up (same
+ * leading dimension), and not otherwise overlap them.  n is a multiple of qa
+ * below 2^31, qa 32, 64 or 128.  gate, up and y rows are 16-byte aligned, q
+ * 8-byte with ld_q a multiple of 16, d 4-byte.  Values are finite, act(gate) *
+ * up too.
  * tokens = 0 does nothing.  Returns BQ_EARG / BQ_EALIGN before any launch, or
  * BQ_EHIP.  Allocates nothing.  Asynchronous on s. */
 typedef struct bq_gated {
